@@ -19,7 +19,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
     "-Xcompiler", "-fPIC", "-shared",
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "--threads", "0",
     "-Xcudafe", "--diag_suppress=20044",
 ]
 
@@ -39,8 +39,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "pha.h"), os.path.abspath(__file__)]
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+        os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -69,12 +69,12 @@ def files_sha(rel_paths) -> str:
 
 
 def sources_sha() -> str:
-    """sha256 over the kernel sources and the ABI header (identifies a kernel build)."""
+    """sha256 over the kernel sources and the ABI headers (identifies a kernel build)."""
     import hashlib
 
     h = hashlib.sha256()
-    for p in sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-            os.path.join(ROOT, "include", "pha.h")]:
+    for p in sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
+            glob.glob(os.path.join(ROOT, "include", "*.h"))):
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode() + b"\0" + f.read())
     return h.hexdigest()[:16]

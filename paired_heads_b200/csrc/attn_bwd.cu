@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
     extern __shared__ float4 bsm4[];
     float* ks = reinterpret_cast<float*>(bsm4);  // [kStage][HP]
     float* vs = ks + kStage * HP;                // [kStage][HP]
-    __shared__ long long range[2];               // keys seen by the block's rows: [min, max)
+    __shared__ long long range[3];               // window keys of the block's rows: [min, max), and
+                                                 // the start of its first document
     const int H = p.heads, Hkv = p.kv_heads, hd = p.head_dim, G = H / Hkv;
     const int64_t slots = static_cast<int64_t>(p.total_tokens) * p.slot_mult;
     const int h = blockIdx.y, g = h / G;
@@ -168,13 +169,14 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
         }
     }
     if (threadIdx.x == 0) {
-        range[0] = LLONG_MAX;
+        range[0] = range[2] = LLONG_MAX;
         range[1] = LLONG_MIN;
     }
     __syncthreads();
     if (in_doc && r8 == 0) {
         atomicMin(&range[0], j0);
         atomicMax(&range[1], j1);
+        atomicMin(&range[2], static_cast<long long>(lo));
     }
     const int64_t row = i * H + h;
     float4 qi[NC], gi[NC], acc[NC];
@@ -187,18 +189,24 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
     warp_range(wj0, wj1);
     __syncthreads();
     const long long J0 = range[0], J1 = range[1];
+    // Sinks below every row's window: those of the block's first document (any later document
+    // starts inside the block, so its sinks are window keys of some row or lie in [J0, J1)).
+    const long long E0 = p.sinks > 0 ? range[2] : J0;
+    const long long E1 = min(E0 + p.sinks, J0);
     const T* kg = static_cast<const T*>(p.k) + static_cast<int64_t>(g) * hd;
     const T* vg = static_cast<const T*>(p.v) + static_cast<int64_t>(g) * hd;
     const int64_t kstride = static_cast<int64_t>(Hkv) * hd;
     const float d = in_doc ? dsum[row] : 0.f;
     {
-        for (long long c0 = J0; c0 < J1; c0 += kStage) {
-            const int n = static_cast<int>(J1 - c0 < kStage ? J1 - c0 : kStage);
+        int n;
+        for (long long c0 = E0 < E1 ? E0 : J0; c0 < J1; c0 = (c0 < E1 && c0 + n >= E1) ? J0 : c0 + n) {
+            const long long end = c0 < E1 ? E1 : J1;
+            n = static_cast<int>(end - c0 < kStage ? end - c0 : kStage);
             __syncthreads();  // every warp is done with the previous chunk
             stage_rows<HP>(ks, kg, c0, n, kstride, hd);
             stage_rows<HP>(vs, vg, c0, n, kstride, hd);
             __syncthreads();
-            if (c0 + n <= wj0 || c0 >= wj1) continue;  // warp-uniform
+            if ((c0 + n <= wj0 && p.sinks == 0) || c0 >= wj1) continue;  // warp-uniform
             for (int jj = 0; jj < n; ++jj) {
                 const long long j = c0 + jj;
                 const float4* kr = reinterpret_cast<const float4*>(ks + jj * HP);
@@ -212,7 +220,8 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
                     dp = dot4(gi[t], vr[r8 + kLanesPerRow * t], dp);
                 }
                 group_sum2(s, dp);
-                const float pij = (j >= j0 && j < j1) ? exp2f(fmaf(s, scale2, -lse2)) : 0.f;
+                const bool vis = j < j1 && (j >= j0 || (j >= lo && j < lo + p.sinks));
+                const float pij = vis ? exp2f(fmaf(s, scale2, -lse2)) : 0.f;
                 const float ds = pij * (dp - d) * p.scale;
 #pragma unroll
                 for (int t = 0; t < NC; ++t) axpy4(acc[t], ds, kk[t]);
@@ -249,7 +258,8 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
         i1 = hi;
         if (p.causal) {
             i0 = j;
-            if (p.window > 0 && j + p.window < i1) i1 = j + p.window;
+            // (a sink is seen by every later query of its document)
+            if (p.window > 0 && j - lo >= p.sinks && j + p.window < i1) i1 = j + p.window;
         }
     }
     if (threadIdx.x == 0) {

@@ -67,6 +67,8 @@ struct AttnProblem {
     int head_dim;
     int causal;
     int window;
+    int sinks;            // first slots of a document that every later query sees (backward only;
+                          // 0: none)
     float scale;
     void* o;
     float* lse;

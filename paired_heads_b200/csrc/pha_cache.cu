@@ -1,0 +1,340 @@
+// pha_cache.cu -- the extern "C" boundary of the serving side (declared in include/pha_cache.h):
+// argument checks, workspace layouts, launches.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/pha_cache.h"
+#include "cache.cuh"
+#include "gather.cuh"
+#include "kernels.cuh"
+
+using namespace pha;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+size_t padded(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// log2 of a power of two, -1 of anything else.
+int log2_exact(int n) {
+    if (n <= 0 || (n & (n - 1)) != 0) return -1;
+    int s = 0;
+    while ((1 << s) < n) ++s;
+    return s;
+}
+
+pha_status of(cudaError_t e) { return e == cudaSuccess ? PHA_OK : PHA_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+pha_status pha_cache_append(const void* k, const void* v, void* k_pages, void* v_pages,
+                            const int32_t* page_table, int max_pages, int n_pages, int page_size,
+                            const int32_t* cu_seqlens, const int32_t* kv_lens, int batch, int total,
+                            int n_kv_heads, int head_dim, int element_bytes, int32_t* status,
+                            pha_stream_t stream) {
+    const int shift = log2_exact(page_size);
+    if (batch <= 0 || total < 0 || max_pages <= 0 || n_pages <= 0 || n_kv_heads <= 0 || head_dim <= 0 ||
+        shift < 0 || (element_bytes != 1 && element_bytes != 2 && element_bytes != 4) ||
+        !aligned(status, 4))
+        return PHA_ERR_INVALID;
+    const int64_t row = static_cast<int64_t>(n_kv_heads) * head_dim * element_bytes;
+    if (row % 16 != 0 || row > (1 << 30) ||
+        (static_cast<int64_t>(n_pages) << shift) * n_kv_heads > INT32_MAX)
+        return PHA_ERR_INVALID;
+    if (total == 0) return PHA_OK;
+    if (!k || !v || !k_pages || !v_pages || !page_table || !cu_seqlens || !kv_lens || !aligned(k, 16) ||
+        !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(page_table, 4) ||
+        !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
+        return PHA_ERR_INVALID;
+    AppendArgs a{};
+    a.k = static_cast<const uint4*>(k);
+    a.v = static_cast<const uint4*>(v);
+    a.k_pages = static_cast<uint4*>(k_pages);
+    a.v_pages = static_cast<uint4*>(v_pages);
+    a.table = page_table;
+    a.cu = cu_seqlens;
+    a.kv_lens = kv_lens;
+    a.status = status;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.page_shift = shift;
+    a.batch = batch;
+    a.total = total;
+    a.row_units = static_cast<int>(row / 16);
+    return of(launch_cache_append(a, stream));
+}
+
+size_t pha_cache_workspace_bytes(int n_pages, int n_seqs) {
+    if (n_pages <= 0 || n_seqs <= 0) return 0;
+    const size_t seqs = padded(sizeof(int32_t) * static_cast<size_t>(n_seqs));
+    const size_t pages = padded(sizeof(int32_t) * static_cast<size_t>(n_pages));
+    return kWorkspaceHeaderBytes + 3 * seqs + 2 * (seqs > pages ? seqs : pages) + pages;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks what the four workspace calls share and lays the workspace out. n: length of the lists.
+pha_status cache_args(CacheArgs& c, int32_t* table, int max_pages, int32_t* lens, int n_seqs,
+                      int32_t* refs, int n_pages, int n, void* workspace, size_t workspace_bytes,
+                      int32_t* status) {
+    if (!table || !refs || !aligned(table, 4) || !aligned(lens, 4) || !aligned(refs, 4) ||
+        !aligned(status, 4) || max_pages <= 0 || n_seqs <= 0 || n_pages <= 0 || n < 0 || n > n_seqs)
+        return PHA_ERR_INVALID;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < pha_cache_workspace_bytes(n_pages, n_seqs))
+        return PHA_ERR_WORKSPACE;
+    c = CacheArgs{};
+    c.table = table;
+    c.lens = lens;
+    c.refs = refs;
+    c.status = status;
+    c.max_pages = max_pages;
+    c.n_seqs = n_seqs;
+    c.n_pages = n_pages;
+    const size_t seqs = padded(sizeof(int32_t) * static_cast<size_t>(n_seqs));
+    const size_t pages = padded(sizeof(int32_t) * static_cast<size_t>(n_pages));
+    const size_t both = seqs > pages ? seqs : pages;
+    auto* w = static_cast<uint8_t*>(workspace);
+    c.hdr = reinterpret_cast<CacheHeader*>(w);
+    w += kWorkspaceHeaderBytes;
+    c.marks = reinterpret_cast<int32_t*>(w);
+    c.need = reinterpret_cast<int32_t*>(w + seqs);
+    c.first = reinterpret_cast<int32_t*>(w + 2 * seqs);
+    c.copy_src = reinterpret_cast<int32_t*>(w + 3 * seqs);
+    c.copy_dst = reinterpret_cast<int32_t*>(w + 3 * seqs + both);
+    c.pages = reinterpret_cast<int32_t*>(w + 3 * seqs + 2 * both);
+    return PHA_OK;
+}
+
+bool bad_list(const int32_t* list, int n) { return n > 0 && (!list || !aligned(list, 4)); }
+
+bool bad_pools(const void* k_cache, const void* v_cache, int n_layers, size_t page_bytes) {
+    return !k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16) || n_layers <= 0 ||
+           page_bytes == 0 || page_bytes % 16 != 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+pha_status pha_cache_fork(int32_t* page_table, int max_pages, int32_t* kv_lens, int n_seqs,
+                          int32_t* page_refs, int n_pages, const int32_t* src, const int32_t* dst,
+                          int n, void* workspace, size_t workspace_bytes, int32_t* status,
+                          pha_stream_t stream) {
+    if (!kv_lens || bad_list(src, n) || bad_list(dst, n)) return PHA_ERR_INVALID;
+    CacheArgs c;
+    const pha_status st = cache_args(c, page_table, max_pages, kv_lens, n_seqs, page_refs, n_pages, n,
+                                     workspace, workspace_bytes, status);
+    return st != PHA_OK ? st : of(launch_cache_fork(c, src, dst, n, stream));
+}
+
+pha_status pha_cache_reserve(int32_t* page_table, int max_pages, int32_t* kv_lens, int n_seqs,
+                             int32_t* page_refs, int n_pages, int page_size, const int32_t* seqs,
+                             const int32_t* new_tokens, int n, void* k_cache, void* v_cache,
+                             int n_layers, size_t page_bytes, void* workspace,
+                             size_t workspace_bytes, int32_t* status, pha_stream_t stream) {
+    const int shift = log2_exact(page_size);
+    if (!kv_lens || bad_list(seqs, n) || bad_list(new_tokens, n) || shift < 0 ||
+        bad_pools(k_cache, v_cache, n_layers, page_bytes))
+        return PHA_ERR_INVALID;
+    CacheArgs c;
+    const pha_status st = cache_args(c, page_table, max_pages, kv_lens, n_seqs, page_refs, n_pages, n,
+                                     workspace, workspace_bytes, status);
+    return st != PHA_OK ? st : of(launch_cache_reserve(c, seqs, new_tokens, n, shift, k_cache, v_cache,
+                                                       n_layers, page_bytes, stream));
+}
+
+pha_status pha_cache_free(int32_t* page_table, int max_pages, int32_t* kv_lens, int n_seqs,
+                          int32_t* page_refs, int n_pages, const int32_t* seqs, int n,
+                          void* workspace, size_t workspace_bytes, int32_t* status,
+                          pha_stream_t stream) {
+    if (!kv_lens || bad_list(seqs, n)) return PHA_ERR_INVALID;
+    CacheArgs c;
+    const pha_status st = cache_args(c, page_table, max_pages, kv_lens, n_seqs, page_refs, n_pages, n,
+                                     workspace, workspace_bytes, status);
+    return st != PHA_OK ? st : of(launch_cache_free(c, seqs, n, stream));
+}
+
+pha_status pha_cache_trim(int32_t* page_table, int max_pages, const int32_t* kv_lens, int n_seqs,
+                          int32_t* page_refs, int n_pages, int page_size, int window, int sinks,
+                          int paired, int32_t* status, pha_stream_t stream) {
+    if (!page_table || !kv_lens || !page_refs || !aligned(page_table, 4) || !aligned(kv_lens, 4) ||
+        !aligned(page_refs, 4) || !aligned(status, 4) || max_pages <= 0 || n_seqs <= 0 || n_pages <= 0 ||
+        log2_exact(page_size) < 0 || window <= 0 || sinks < 0 || (paired != 0 && paired != 1) ||
+        (static_cast<int64_t>(n_seqs) * max_pages + 255) / 256 > INT32_MAX)
+        return PHA_ERR_INVALID;
+    CacheArgs c{};
+    c.table = page_table;
+    c.lens = const_cast<int32_t*>(kv_lens);
+    c.refs = page_refs;
+    c.status = status;
+    c.max_pages = max_pages;
+    c.n_seqs = n_seqs;
+    c.n_pages = n_pages;
+    return of(launch_cache_trim(c, page_size, window, sinks, paired ? 2 : 1, stream));
+}
+
+pha_status pha_cache_compact(int32_t* page_table, int max_pages, int n_seqs, int32_t* page_refs,
+                             int n_pages, void* k_cache, void* v_cache, int n_layers,
+                             size_t page_bytes, void* workspace, size_t workspace_bytes,
+                             int32_t* status, pha_stream_t stream) {
+    if (bad_pools(k_cache, v_cache, n_layers, page_bytes)) return PHA_ERR_INVALID;
+    CacheArgs c;
+    const pha_status st = cache_args(c, page_table, max_pages, nullptr, n_seqs, page_refs, n_pages, 0,
+                                     workspace, workspace_bytes, status);
+    return st != PHA_OK ? st : of(launch_cache_compact(c, k_cache, v_cache, n_layers, page_bytes, stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------ paged attention
+
+namespace {
+
+constexpr int kRowsSplitKeys = 1024;  // key columns of one warp's split (float32)
+constexpr int kGpuSms = 148;          // workspaces may not depend on the device at hand
+constexpr int kMinSplitTiles = 4;     // key tiles of a split of the tensor-core kernel, at least
+
+struct PagedPlan {
+    bool gather;                 // the tensor-core kernel with a work list
+    int n_splits, split_keys;
+    int pack, tile_tokens;
+    int64_t items;
+    size_t before, list, part_o, part_lse, bytes;  // workspace offsets
+};
+
+// The path, the splits and the workspace of a paged call. false: arguments out of range.
+bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int n_heads,
+                int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks, int paired) {
+    if (batch <= 0 || max_q < 0 || max_kv < 0 || total_q < 0 || total_q > (1 << 28) ||
+        max_kv > (1 << 29) || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
+        n_heads % n_kv_heads != 0 || head_dim <= 0 || head_dim > 128 || sinks < 0 ||
+        (paired != 0 && paired != 1) || (paired && ((n_heads & 1) || (n_kv_heads & 1))))
+        return false;
+    const int mult = paired ? 2 : 1;
+    const int heads = n_heads / mult, kv_heads = n_kv_heads / mult;
+    // the most key columns the new tokens of one sequence can see
+    int64_t most = static_cast<int64_t>(max_kv) * mult;
+    if (window > 0) {
+        const int64_t seen = static_cast<int64_t>(window) + static_cast<int64_t>(max_q) * mult + sinks;
+        most = seen < most ? seen : most;
+    }
+    w = PagedPlan{};
+    w.gather = dtype == PHA_BF16;
+    if (w.gather) {
+        w.pack = gather_pack(heads, kv_heads);
+        w.tile_tokens = gather_tile_tokens(w.pack, window, sinks);
+        const int64_t base = gather_items(batch, static_cast<int64_t>(max_q) * mult,
+                                          static_cast<int64_t>(total_q) * mult, w.tile_tokens, heads / w.pack, 1);
+        // few row tiles: split their key tiles so that every SM has an item
+        const int64_t tiles = (most + kBlockN - 1) / kBlockN;
+        int64_t s = base > 0 ? kGpuSms / base : 1;
+        if (s > tiles / kMinSplitTiles) s = tiles / kMinSplitTiles;
+        w.n_splits = s < 1 ? 1 : static_cast<int>(s);
+        w.items = base * w.n_splits;
+        if (w.items > INT32_MAX) return false;
+    } else {
+        w.split_keys = kRowsSplitKeys;
+        w.n_splits = static_cast<int>((most + w.split_keys - 1) / w.split_keys);
+        if (w.n_splits < 1) w.n_splits = 1;
+    }
+    const size_t rows = static_cast<size_t>(total_q) * n_heads;
+    const size_t parts = w.n_splits > 1 ? rows * w.n_splits : 0;
+    w.before = kWorkspaceHeaderBytes;
+    w.list = w.before + (w.gather ? padded(sizeof(int) * (static_cast<size_t>(batch) + 1)) : 0);
+    w.part_o = w.list + padded(2 * sizeof(int4) * static_cast<size_t>(w.items));
+    w.part_lse = w.part_o + padded(parts * head_dim * sizeof(float));
+    w.bytes = w.part_lse + padded(parts * sizeof(float));
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pha_attn_paged_workspace_bytes(int batch, int max_q, int max_kv, int total_q, int n_heads,
+                                      int n_kv_heads, int head_dim, pha_dtype dtype, int window,
+                                      int sinks, int paired) {
+    PagedPlan w;
+    if (dtype != PHA_BF16 && dtype != PHA_F32) return 0;
+    return paged_plan(w, batch, max_q, max_kv, total_q, n_heads, n_kv_heads, head_dim, dtype, window,
+                      sinks, paired)
+               ? w.bytes
+               : 0;
+}
+
+pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* page_table, int max_pages, int n_pages, int page_size,
+                              const int32_t* cu_seqlens, const int32_t* kv_lens, int batch,
+                              int max_q, int max_kv, int total_q, int n_heads, int n_kv_heads,
+                              int head_dim, pha_dtype dtype, int window, int sinks, int paired,
+                              float scale, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, int32_t* status, pha_stream_t stream) {
+    const int shift = log2_exact(page_size);
+    if ((dtype != PHA_BF16 && dtype != PHA_F32) || shift < 0 || shift > 24 || n_pages <= 0 ||
+        max_pages <= 0 || !(scale == scale) || !aligned(status, 4) || !aligned(lse, 4))
+        return PHA_ERR_INVALID;
+    if (head_dim > 128) return PHA_ERR_UNSUPPORTED;
+    PagedPlan w;
+    if (!paged_plan(w, batch, max_q, max_kv, total_q, n_heads, n_kv_heads, head_dim, dtype, window,
+                    sinks, paired) ||
+        (static_cast<int64_t>(n_pages) << shift) * n_kv_heads > INT32_MAX)
+        return PHA_ERR_INVALID;
+    if (dtype == PHA_BF16 && head_dim != 64 && head_dim != 128) return PHA_ERR_UNSUPPORTED;
+    if (total_q == 0) return PHA_OK;
+    if (!q || !k_pages || !v_pages || !o || !page_table || !cu_seqlens || !kv_lens || !aligned(q, 16) ||
+        !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) || !aligned(page_table, 4) ||
+        !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
+        return PHA_ERR_INVALID;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes) return PHA_ERR_WORKSPACE;
+    GatherProblem p{};
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.o = o;
+    p.lse = lse;
+    p.cu = cu_seqlens;
+    p.kv_lens = kv_lens;
+    p.table = page_table;
+    p.max_pages = max_pages;
+    p.n_pages = n_pages;
+    p.mult = paired ? 2 : 1;
+    p.page_shift = shift + (paired ? 1 : 0);
+    p.batch = batch;
+    p.max_q = max_q;
+    p.max_kv = max_kv;
+    p.total_q = total_q;
+    p.heads = n_heads / p.mult;
+    p.kv_heads = n_kv_heads / p.mult;
+    p.head_dim = head_dim;
+    p.window = window > 0 ? window : 0;
+    p.sinks = sinks;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    p.n_splits = w.n_splits;
+    p.split_keys = w.split_keys;
+    auto* base = static_cast<uint8_t*>(workspace);
+    p.part_o = reinterpret_cast<float*>(base + w.part_o);
+    p.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+    p.status = status;
+    p.pack = w.pack;
+    p.tile_tokens = w.tile_tokens;
+    cudaError_t e;
+    if (w.gather) {
+        p.hdr = reinterpret_cast<WorkspaceHeader*>(base);
+        p.items = reinterpret_cast<int4*>(base + w.list);
+        e = launch_gather_plan(p, w.items, reinterpret_cast<int*>(base + w.before), false, stream);
+        if (e == cudaSuccess) e = launch_attn_gather(p, w.items, stream);
+    } else {
+        e = launch_attn_rows(p, stream);
+    }
+    if (e == cudaSuccess && p.n_splits > 1) e = launch_attn_join(p, dtype == PHA_BF16, stream);
+    return of(e);
+}
+
+}  // extern "C"

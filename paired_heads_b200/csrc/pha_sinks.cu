@@ -1,0 +1,158 @@
+// pha_sinks.cu -- the extern "C" boundary of attention with a sliding window and sinks (declared in
+// include/pha_sinks.h): argument checks, workspace layouts, launches.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/pha_sinks.h"
+#include "gather.cuh"
+#include "kernels.cuh"
+
+using namespace pha;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+pha_status of(cudaError_t e) { return e == cudaSuccess ? PHA_OK : PHA_ERR_CUDA; }
+
+// Shape checks of both directions.
+pha_status shape_status(int batch, int max_len, int total_tokens, int n_heads, int n_kv_heads,
+                        int head_dim, pha_dtype dtype, int sinks, int paired, float scale) {
+    if ((dtype != PHA_BF16 && dtype != PHA_F32) || batch <= 0 || max_len < 0 || total_tokens < 0 ||
+        total_tokens > (1 << 29) || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
+        n_heads % n_kv_heads != 0 || head_dim <= 0 || sinks < 0 || (paired != 0 && paired != 1) ||
+        !(scale == scale) || (paired && ((n_heads & 1) || (n_kv_heads & 1))))
+        return PHA_ERR_INVALID;
+    if (sinks > kBlockN || head_dim > 128 || (dtype == PHA_BF16 && head_dim != 64 && head_dim != 128))
+        return PHA_ERR_UNSUPPORTED;
+    return PHA_OK;
+}
+
+size_t padded(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Work items of the forward (documents of any lengths up to max_len).
+int64_t fwd_items(int batch, int max_len, int n_heads, int n_kv_heads, int window, int sinks, int paired) {
+    const int mult = paired ? 2 : 1, heads = n_heads / mult;
+    const int pack = gather_pack(heads, n_kv_heads / mult);
+    const int64_t slots = static_cast<int64_t>(max_len) * mult;
+    return gather_items(batch, slots, slots * batch, gather_tile_tokens(pack, window, sinks), heads / pack, 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pha_attn_sinks_workspace_bytes(int batch, int max_len, int n_heads, int n_kv_heads,
+                                      int head_dim, int window, int sinks, int paired) {
+    if (shape_status(batch, max_len, 0, n_heads, n_kv_heads, head_dim, PHA_F32, sinks, paired, 0.f) != PHA_OK)
+        return 0;
+    return kWorkspaceHeaderBytes + padded(sizeof(int) * (static_cast<size_t>(batch) + 1)) +
+           2 * sizeof(int4) * static_cast<size_t>(fwd_items(batch, max_len, n_heads, n_kv_heads, window, sinks, paired));
+}
+
+size_t pha_attn_sinks_bwd_workspace_bytes(int batch, int max_len, int total_tokens, int n_heads,
+                                          int n_kv_heads, int head_dim, int window, int sinks,
+                                          int paired) {
+    (void)window;
+    if (shape_status(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, PHA_F32, sinks, paired,
+                     0.f) != PHA_OK)
+        return 0;
+    return pha_attn_bwd_workspace_bytes(batch, max_len, total_tokens, n_heads, head_dim, paired);
+}
+
+pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
+                              const int32_t* cu_seqlens, int batch, int max_len, int total_tokens,
+                              int n_heads, int n_kv_heads, int head_dim, pha_dtype dtype,
+                              int window, int sinks, int paired, float scale, void* o, float* lse,
+                              void* workspace, size_t workspace_bytes, pha_stream_t stream) {
+    const pha_status st = shape_status(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, dtype,
+                                       sinks, paired, scale);
+    if (st != PHA_OK) return st;
+    const bool have = total_tokens > 0;
+    if ((have && (!q || !k || !v || !o || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+                  !aligned(o, 16))) ||
+        !cu_seqlens || !aligned(cu_seqlens, 4) || !aligned(lse, 4))
+        return PHA_ERR_INVALID;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < pha_attn_sinks_workspace_bytes(batch, max_len, n_heads, n_kv_heads, head_dim,
+                                                         window, sinks, paired))
+        return PHA_ERR_WORKSPACE;
+    GatherProblem p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.o = o;
+    p.lse = lse;
+    p.cu = cu_seqlens;
+    p.batch = batch;
+    p.max_q = p.max_kv = max_len;
+    p.total_q = total_tokens;
+    p.mult = paired ? 2 : 1;
+    p.heads = n_heads / p.mult;
+    p.kv_heads = n_kv_heads / p.mult;
+    p.head_dim = head_dim;
+    p.window = window > 0 ? window : 0;
+    p.sinks = sinks;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    p.n_splits = 1;
+    p.pack = gather_pack(p.heads, p.kv_heads);
+    p.tile_tokens = gather_tile_tokens(p.pack, p.window, p.sinks);
+    auto* base = static_cast<uint8_t*>(workspace);
+    p.hdr = reinterpret_cast<WorkspaceHeader*>(base);
+    auto* before = reinterpret_cast<int*>(base + kWorkspaceHeaderBytes);
+    const bool tc = dtype == PHA_BF16;
+    if (tc)
+        p.items = reinterpret_cast<int4*>(base + kWorkspaceHeaderBytes +
+                                          padded(sizeof(int) * (static_cast<size_t>(batch) + 1)));
+    const int64_t items = fwd_items(batch, max_len, n_heads, n_kv_heads, window, sinks, paired);
+    cudaError_t e = launch_gather_plan(p, items < INT32_MAX ? items : INT32_MAX, before, true, stream);
+    if (e == cudaSuccess && have) e = tc ? launch_attn_gather(p, items, stream) : launch_attn_rows(p, stream);
+    return of(e);
+}
+
+pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const void* o,
+                              const float* lse, const void* dout, const int32_t* cu_seqlens,
+                              int batch, int max_len, int total_tokens, int n_heads,
+                              int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks,
+                              int paired, float scale, void* dq, void* dk, void* dv,
+                              void* workspace, size_t workspace_bytes, pha_stream_t stream) {
+    const pha_status st = shape_status(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, dtype,
+                                       sinks, paired, scale);
+    if (st != PHA_OK) return st;
+    const bool have = total_tokens > 0;
+    if ((have && (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !aligned(q, 16) ||
+                  !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dout, 16) ||
+                  !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4))) ||
+        !cu_seqlens || !aligned(cu_seqlens, 4))
+        return PHA_ERR_INVALID;
+    if (!have) return PHA_OK;  // nothing to do (no launch, the workspace is not touched)
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < pha_attn_sinks_bwd_workspace_bytes(batch, max_len, total_tokens, n_heads,
+                                                             n_kv_heads, head_dim, window, sinks, paired))
+        return PHA_ERR_WORKSPACE;
+    AttnProblem p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.cu_seqlens = cu_seqlens;
+    p.batch = batch;
+    p.max_len = max_len;
+    p.total_tokens = total_tokens;
+    p.slot_mult = paired ? 2 : 1;
+    p.heads = n_heads / p.slot_mult;
+    p.kv_heads = n_kv_heads / p.slot_mult;
+    p.head_dim = head_dim;
+    p.causal = 1;
+    p.window = window > 0 ? window : 0;
+    p.sinks = p.window > 0 ? sinks : 0;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    p.lse = const_cast<float*>(lse);
+    auto* base = static_cast<uint8_t*>(workspace);
+    float* dsum = reinterpret_cast<float*>(base + kWorkspaceHeaderBytes);
+    if (launch_attn_bwd_dsum(p, o, dout, dsum, dtype == PHA_BF16, stream) != cudaSuccess)
+        return PHA_ERR_CUDA;
+    return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, dtype == PHA_BF16, stream));
+}
+
+}  // extern "C"

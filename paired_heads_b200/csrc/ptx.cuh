@@ -8,8 +8,15 @@
 
 namespace pha {
 
-// Device-side status codes (written into the workspace header).
-enum : int { DEV_OK = 0, DEV_BAD_SEQLENS = 1, DEV_OVERFLOW = 2, DEV_TIMEOUT = 3 };
+// Device-side status codes (written into the workspace header or a caller's status word).
+enum : int {
+    DEV_OK = 0,
+    DEV_BAD_SEQLENS = 1,
+    DEV_OVERFLOW = 2,
+    DEV_TIMEOUT = 3,
+    DEV_BAD_PAGE = 4,   // a needed page table entry is no page
+    DEV_NO_PAGES = 5    // not enough free pages
+};
 
 // A wait gives up after this many nanoseconds of %globaltimer time.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
@@ -95,6 +102,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // thread waits only for its own copies (a hardware wait, not a spin).
 __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gsrc) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gsrc)
+                 : "memory");
+}
+// The same, copying only the first `bytes` (0 or 16) and filling the rest with zeros; the source is
+// not read for bytes = 0 but must be a valid address.
+__device__ __forceinline__ void cp_async_16_zfill(uint32_t smem_dst, const void* gsrc, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {

@@ -1,5 +1,5 @@
-"""ctypes binding of libpha (include/pha.h). Argument marshalling only: every step runs in the
-library's CUDA kernels. Importing this module loads libpha.so and raises if it is missing -- there
+"""ctypes binding of libpha (include/pha.h, include/pha_sinks.h, include/pha_cache.h). Argument
+marshalling only: every step runs in the library's CUDA kernels. Importing this module loads libpha.so and raises if it is missing -- there
 is no fallback.
 
 Functions keep the C names. Tensor arguments may be torch tensors (their device pointer is
@@ -15,12 +15,15 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpha.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "pha.h")
+HEADERS = [HEADER] + [os.path.join(os.path.dirname(HERE), "include", n)
+                      for n in ("pha_sinks.h", "pha_cache.h")]
 
 PHA_BF16 = 0
 PHA_F32 = 1
 STATUS = {0: "PHA_OK", -1: "PHA_ERR_INVALID", -2: "PHA_ERR_UNSUPPORTED", -3: "PHA_ERR_WORKSPACE",
           -4: "PHA_ERR_CUDA"}
-DEVICE_STATUS = {0: "ok", 1: "malformed cu_seqlens", 2: "work list overflow", 3: "wait timeout"}
+DEVICE_STATUS = {0: "ok", 1: "malformed cu_seqlens", 2: "work list overflow", 3: "wait timeout",
+                 4: "page table entry is no page", 5: "not enough free pages"}
 
 
 class PhaError(RuntimeError):
@@ -69,6 +72,30 @@ _lib.pha_rope_factored.argtypes = [_p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _i, _
 _lib.pha_rope_bwd_factored.argtypes = [_p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _i, _i, _p]
 _lib.pha_qk_norm_rope_factored.argtypes = [_p, _p, _p, _p, ctypes.c_float, _p, _i, _p, _i, _i, _i,
                                            _i, _i, _i, _i, _p]
+_f32 = ctypes.c_float
+_lib.pha_attn_sinks_workspace_bytes.argtypes = [_i] * 8
+_lib.pha_attn_sinks_workspace_bytes.restype = _sz
+_lib.pha_attn_sinks_bwd_workspace_bytes.argtypes = [_i] * 9
+_lib.pha_attn_sinks_bwd_workspace_bytes.restype = _sz
+_lib.pha_attn_sinks_fwd.argtypes = [_p] * 4 + [_i] * 10 + [_f32, _p, _p, _p, _sz, _p]
+_lib.pha_attn_sinks_bwd.argtypes = [_p] * 7 + [_i] * 10 + [_f32, _p, _p, _p, _p, _sz, _p]
+_lib.pha_attn_paged_workspace_bytes.argtypes = [_i] * 11
+_lib.pha_attn_paged_workspace_bytes.restype = _sz
+_lib.pha_attn_paged_fwd.argtypes = [_p] * 4 + [_i] * 3 + [_p, _p] + [_i] * 11 + [_f32, _p, _p, _p,
+                                                                               _sz, _p, _p]
+_lib.pha_cache_append.argtypes = [_p] * 5 + [_i] * 3 + [_p, _p] + [_i] * 5 + [_p, _p]
+_lib.pha_cache_workspace_bytes.argtypes = [_i, _i]
+_lib.pha_cache_workspace_bytes.restype = _sz
+_lib.pha_cache_fork.argtypes = [_p, _i, _p, _i, _p, _i, _p, _p, _i, _p, _sz, _p, _p]
+_lib.pha_cache_reserve.argtypes = [_p, _i, _p, _i, _p, _i, _i, _p, _p, _i, _p, _p, _i, _sz, _p, _sz,
+                                   _p, _p]
+_lib.pha_cache_free.argtypes = [_p, _i, _p, _i, _p, _i, _p, _i, _p, _sz, _p, _p]
+_lib.pha_cache_trim.argtypes = [_p, _i, _p, _i, _p] + [_i] * 5 + [_p, _p]
+_lib.pha_cache_compact.argtypes = [_p, _i, _i, _p, _i, _p, _p, _i, _sz, _p, _sz, _p, _p]
+for _f in ("pha_attn_sinks_fwd", "pha_attn_sinks_bwd", "pha_attn_paged_fwd", "pha_cache_append",
+           "pha_cache_fork", "pha_cache_reserve", "pha_cache_free", "pha_cache_trim",
+           "pha_cache_compact"):
+    getattr(_lib, _f).restype = _i
 for _f in ("pha_rope_tables", "pha_rope", "pha_attn_fwd", "pha_attn_status",
            "pha_attn_fwd_noalloc", "pha_test_attn_fwd_stalled", "pha_attn_fwd_fp8", "pha_qk_norm_rope", "pha_attn_fwd_aux_v", "pha_rope_bwd",
            "pha_attn_bwd", "pha_rope_factor_tables", "pha_rope_factored", "pha_rope_bwd_factored",
@@ -77,10 +104,13 @@ for _f in ("pha_rope_tables", "pha_rope", "pha_attn_fwd", "pha_attn_status",
 
 
 def exported_symbols() -> list:
-    """Names of the functions include/pha.h declares."""
-    with open(HEADER) as f:
-        text = f.read()
-    return sorted(set(re.findall(r"^\s*(?:const\s+)?[\w\s\*]+?\b(pha_\w+)\s*\(", text, re.M)))
+    """Names of the functions the headers declare."""
+    names = set()
+    for path in HEADERS:
+        with open(path) as f:
+            text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+        names.update(re.findall(r"^\s*(?:const\s+)?[\w\s\*]+?\b(pha_\w+)\s*\(", text, re.M))
+    return sorted(names)
 
 
 def library():
@@ -357,3 +387,252 @@ def pha_attn_status(workspace, stream=None):
     _check("pha_attn_status", _lib.pha_attn_status(_ptr(workspace), ctypes.byref(st),
                                                    ctypes.byref(n), _stream(stream, workspace)))
     return st.value, n.value
+
+
+# ---------------------------------------------------------------- sinks and the paged cache
+#
+# These take torch tensors only, and check what the C side cannot see: types, shapes, devices and
+# that the elements are contiguous. A tensor on another device than the current one is fine: the
+# call is made on the tensor's device.
+
+def _want(name, t, dtype, *shape):
+    """t is a contiguous tensor of this dtype and shape (None: any extent)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+
+
+def _run(fn, args, stream, first, *others):
+    """Calls the library on the device of `first`, which the other tensors must share."""
+    import torch
+
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: tensors not on a CUDA device")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
+    call = getattr(_lib, fn)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn, call(*args, _stream(stream, first)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, call(*args, _stream(stream, first)))
+
+
+def _int32():
+    import torch
+
+    return torch.int32
+
+
+def _attn_shape(q, k, v, o, lse):
+    """Checks q, k, v, o, lse of a packed call; (tokens, heads, kv heads, head_dim, dtype code)."""
+    import torch
+
+    dt = _dtype_code(q)
+    t, h, hd = q.shape
+    hkv = k.shape[-2]
+    _want("q", q, q.dtype, t, h, hd)
+    _want("o", o, q.dtype, t, h, hd)
+    if lse is not None:
+        _want("lse", lse, torch.float32, t, h)
+    return t, h, hkv, hd, dt
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def pha_attn_sinks_workspace_bytes(batch: int, max_len: int, n_heads: int, n_kv_heads: int,
+                                   head_dim: int, *, window: int, sinks: int,
+                                   paired: bool = False) -> int:
+    return int(_lib.pha_attn_sinks_workspace_bytes(batch, max_len, n_heads, n_kv_heads, head_dim,
+                                                   window, sinks, int(paired)))
+
+
+def pha_attn_sinks_bwd_workspace_bytes(batch: int, max_len: int, total_tokens: int, n_heads: int,
+                                       n_kv_heads: int, head_dim: int, *, window: int, sinks: int,
+                                       paired: bool = False) -> int:
+    return int(_lib.pha_attn_sinks_bwd_workspace_bytes(batch, max_len, total_tokens, n_heads,
+                                                       n_kv_heads, head_dim, window, sinks,
+                                                       int(paired)))
+
+
+def pha_attn_sinks_fwd(q, k, v, cu_seqlens, max_len: int, o, lse, workspace, *, window: int,
+                       sinks: int, paired: bool = False, scale: float = 0.0, stream=None):
+    """Causal varlen attention with a sliding window and `sinks` visible first slots per document,
+    into o (like q) and lse [T][H] float32 (or None). pha_attn_status(workspace) reports."""
+    t, h, hkv, hd, dt = _attn_shape(q, k, v, o, lse)
+    _want("k", k, q.dtype, t, hkv, hd)
+    _want("v", v, q.dtype, t, hkv, hd)
+    _want("cu_seqlens", cu_seqlens, _int32(), None)
+    _run("pha_attn_sinks_fwd",
+         (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
+          max_len, t, h, hkv, hd, dt, window, sinks, int(paired), scale, o.data_ptr(), _ptr(lse),
+          workspace.data_ptr(), _nbytes(workspace)), stream, q, k, v, cu_seqlens, o, lse, workspace)
+
+
+def pha_attn_sinks_bwd(q, k, v, o, lse, dout, cu_seqlens, max_len: int, dq, dk, dv, workspace, *,
+                       window: int, sinks: int, paired: bool = False, scale: float = 0.0,
+                       stream=None):
+    """Backward of pha_attn_sinks_fwd (o, lse: its outputs): dq, dk, dv for dout."""
+    t, h, hkv, hd, dt = _attn_shape(q, k, v, o, lse)
+    for name, x, heads in (("k", k, hkv), ("v", v, hkv), ("dout", dout, h), ("dq", dq, h),
+                           ("dk", dk, hkv), ("dv", dv, hkv)):
+        _want(name, x, q.dtype, t, heads, hd)
+    _want("cu_seqlens", cu_seqlens, _int32(), None)
+    _run("pha_attn_sinks_bwd",
+         (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), dout.data_ptr(),
+          cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, max_len, t, h, hkv, hd, dt, window, sinks,
+          int(paired), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+          _nbytes(workspace)), stream, q, k, v, o, lse, dout, cu_seqlens, dq, dk, dv, workspace)
+
+
+def pha_attn_paged_workspace_bytes(batch: int, max_q: int, max_kv: int, total_q: int, n_heads: int,
+                                   n_kv_heads: int, head_dim: int, dtype, *, window: int = 0,
+                                   sinks: int = 0, paired: bool = False) -> int:
+    """dtype: torch.bfloat16 or torch.float32."""
+    import torch
+
+    code = PHA_BF16 if dtype == torch.bfloat16 else PHA_F32
+    return int(_lib.pha_attn_paged_workspace_bytes(batch, max_q, max_kv, total_q, n_heads,
+                                                   n_kv_heads, head_dim, code, window, sinks,
+                                                   int(paired)))
+
+
+def pha_attn_paged_fwd(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, max_q: int,
+                       max_kv: int, o, lse, workspace, *, window: int = 0, sinks: int = 0,
+                       paired: bool = False, scale: float = 0.0, status=None, stream=None):
+    """Attention of each sequence's new tokens q over its paged cache (k_pages, v_pages
+    [pages][page_size][Hkv][hd], page_table [batch][max_pages], kv_lens [batch] with the new tokens
+    included) into o and lse (or None). status: int32[1], raised on bad lengths or pages."""
+    t, h, hkv, hd, dt = _attn_shape(q, k_pages, v_pages, o, lse)
+    n_pages, page = k_pages.shape[:2]
+    batch = cu_seqlens.shape[0] - 1
+    _want("k_pages", k_pages, q.dtype, n_pages, page, hkv, hd)
+    _want("v_pages", v_pages, q.dtype, n_pages, page, hkv, hd)
+    i32 = _int32()
+    _want("page_table", page_table, i32, batch, None)
+    _want("cu_seqlens", cu_seqlens, i32, batch + 1)
+    _want("kv_lens", kv_lens, i32, batch)
+    if status is not None:
+        _want("status", status, i32, 1)
+    _run("pha_attn_paged_fwd",
+         (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+          page_table.shape[1], n_pages, page, cu_seqlens.data_ptr(), kv_lens.data_ptr(), batch,
+          max_q, max_kv, t, h, hkv, hd, dt, window, sinks, int(paired), scale, o.data_ptr(),
+          _ptr(lse), workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream, q, k_pages,
+         v_pages, page_table, cu_seqlens, kv_lens, o, lse, workspace, status)
+
+
+def pha_cache_append(k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, *, status=None,
+                     stream=None):
+    """Writes the new tokens' k, v [T][Hkv][hd] to their places in k_pages, v_pages (one layer)."""
+    t, hkv, hd = k.shape
+    n_pages, page = k_pages.shape[:2]
+    batch = cu_seqlens.shape[0] - 1
+    _want("k", k, k.dtype, t, hkv, hd)
+    _want("v", v, k.dtype, t, hkv, hd)
+    _want("k_pages", k_pages, k.dtype, n_pages, page, hkv, hd)
+    _want("v_pages", v_pages, k.dtype, n_pages, page, hkv, hd)
+    i32 = _int32()
+    _want("page_table", page_table, i32, batch, None)
+    _want("cu_seqlens", cu_seqlens, i32, batch + 1)
+    _want("kv_lens", kv_lens, i32, batch)
+    if status is not None:
+        _want("status", status, i32, 1)
+    _run("pha_cache_append",
+         (k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          page_table.data_ptr(), page_table.shape[1], n_pages, page, cu_seqlens.data_ptr(),
+          kv_lens.data_ptr(), batch, t, hkv, hd, k.element_size(), _ptr(status)), stream, k, v,
+         k_pages, v_pages, page_table, cu_seqlens, kv_lens, status)
+
+
+def pha_cache_workspace_bytes(n_pages: int, n_seqs: int) -> int:
+    return int(_lib.pha_cache_workspace_bytes(n_pages, n_seqs))
+
+
+def _cache_state(page_table, kv_lens, page_refs, status):
+    """Checks the bookkeeping tensors; (max_pages, sequences, pages)."""
+    i32 = _int32()
+    n_seqs, max_pages = page_table.shape
+    _want("page_table", page_table, i32, n_seqs, max_pages)
+    if kv_lens is not None:
+        _want("kv_lens", kv_lens, i32, n_seqs)
+    _want("page_refs", page_refs, i32, None)
+    if status is not None:
+        _want("status", status, i32, 1)
+    return max_pages, n_seqs, page_refs.shape[0]
+
+
+def _cache_pools(k_cache, v_cache, n_pages):
+    """Checks pools [layers][pages][page_size][Hkv][hd]; (layers, bytes of one page)."""
+    layers, _, page, hkv, hd = k_cache.shape
+    _want("k_cache", k_cache, k_cache.dtype, layers, n_pages, page, hkv, hd)
+    _want("v_cache", v_cache, k_cache.dtype, layers, n_pages, page, hkv, hd)
+    return layers, page * hkv * hd * k_cache.element_size()
+
+
+def pha_cache_fork(page_table, kv_lens, page_refs, src, dst, workspace, *, status=None,
+                   stream=None):
+    """Empty sequences dst[i] become further holders of src[i]'s pages (nothing is copied)."""
+    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
+    n = src.shape[0]
+    _want("src", src, _int32(), n)
+    _want("dst", dst, _int32(), n)
+    _run("pha_cache_fork",
+         (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg,
+          src.data_ptr(), dst.data_ptr(), n, workspace.data_ptr(), _nbytes(workspace),
+          _ptr(status)), stream, page_table, kv_lens, page_refs, src, dst, workspace, status)
+
+
+def pha_cache_reserve(page_table, kv_lens, page_refs, seqs, new_tokens, k_cache, v_cache, workspace,
+                      *, status=None, stream=None):
+    """Room for new_tokens[i] more tokens of sequence seqs[i]; a shared last page that a sequence
+    grows into is copied (k_cache, v_cache [layers][pages][page_size][Hkv][hd])."""
+    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
+    layers, page_bytes = _cache_pools(k_cache, v_cache, npg)
+    n = seqs.shape[0]
+    _want("seqs", seqs, _int32(), n)
+    _want("new_tokens", new_tokens, _int32(), n)
+    _run("pha_cache_reserve",
+         (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg,
+          k_cache.shape[2], seqs.data_ptr(), new_tokens.data_ptr(), n, k_cache.data_ptr(),
+          v_cache.data_ptr(), layers, page_bytes, workspace.data_ptr(), _nbytes(workspace),
+          _ptr(status)), stream, page_table, kv_lens, page_refs, seqs, new_tokens, k_cache,
+         v_cache, workspace, status)
+
+
+def pha_cache_free(page_table, kv_lens, page_refs, seqs, workspace, *, status=None, stream=None):
+    """Sequences seqs[i] let go of their pages and become empty."""
+    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
+    n = seqs.shape[0]
+    _want("seqs", seqs, _int32(), n)
+    _run("pha_cache_free",
+         (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg,
+          seqs.data_ptr(), n, workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream,
+         page_table, kv_lens, page_refs, seqs, workspace, status)
+
+
+def pha_cache_trim(page_table, kv_lens, page_refs, page_size: int, *, window: int, sinks: int = 0,
+                   paired: bool = False, status=None, stream=None):
+    """Every sequence lets go of the pages that no later token sees with this window and sinks."""
+    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
+    _run("pha_cache_trim",
+         (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg, page_size,
+          window, sinks, int(paired), _ptr(status)), stream, page_table, kv_lens, page_refs, status)
+
+
+def pha_cache_compact(page_table, page_refs, k_cache, v_cache, workspace, *, status=None,
+                      stream=None):
+    """Moves the pages in use together at the front of the pool, in all layers."""
+    mp, ns, npg = _cache_state(page_table, None, page_refs, status)
+    layers, page_bytes = _cache_pools(k_cache, v_cache, npg)
+    _run("pha_cache_compact",
+         (page_table.data_ptr(), mp, ns, page_refs.data_ptr(), npg, k_cache.data_ptr(),
+          v_cache.data_ptr(), layers, page_bytes, workspace.data_ptr(), _nbytes(workspace),
+          _ptr(status)), stream, page_table, page_refs, k_cache, v_cache, workspace, status)

@@ -1,0 +1,224 @@
+"""Argument checks of the sinks and paged-cache entry points: refused on the host, before any CUDA
+call (so they run on CPU), and the binding's checks of types, shapes and layouts."""
+import ctypes
+
+import pytest
+
+from paired_heads_b200 import build as pha_build
+
+A, MIS = 0x10000, 0x10004
+
+
+@pytest.fixture(scope="module")
+def pha():
+    pha_build.build()
+    from paired_heads_b200 import pha as mod
+
+    return mod
+
+
+def test_new_entry_points_are_exported(pha):
+    names = pha.exported_symbols()
+    for n in ("pha_attn_sinks_fwd", "pha_attn_sinks_bwd", "pha_attn_paged_fwd", "pha_cache_append",
+              "pha_cache_fork", "pha_cache_reserve", "pha_cache_free", "pha_cache_trim",
+              "pha_cache_compact", "pha_attn_fwd"):
+        assert n in names
+        assert hasattr(pha.library(), n)
+
+
+def _sinks(pha, bwd=False, **kw):
+    a = dict(q=A, k=A, v=A, cu=A, batch=1, max_len=128, total=128, H=4, Hkv=4, hd=64, dtype=0,
+             window=64, sinks=4, paired=0, scale=0.0, o=A, lse=A, dout=A, dq=A, dk=A, dv=A, ws=A,
+             bytes=10)
+    a.update(kw)
+    f = ctypes.c_float(a["scale"])
+    shape = (a["cu"], a["batch"], a["max_len"], a["total"], a["H"], a["Hkv"], a["hd"], a["dtype"],
+             a["window"], a["sinks"], a["paired"], f)
+    if bwd:
+        return pha.library().pha_attn_sinks_bwd(a["q"], a["k"], a["v"], a["o"], a["lse"], a["dout"],
+                                                *shape, a["dq"], a["dk"], a["dv"], a["ws"],
+                                                a["bytes"], None)
+    return pha.library().pha_attn_sinks_fwd(a["q"], a["k"], a["v"], *shape, a["o"], a["lse"],
+                                            a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("kw,code", [
+    ({}, -3),                                  # a valid problem: only the workspace is too small
+    (dict(sinks=128), -3),
+    (dict(window=0), -3),                      # no window: the sinks change nothing
+    (dict(ws=None, bytes=1 << 30), -3),
+    (dict(ws=MIS, bytes=1 << 30), -3),
+    (dict(sinks=-1), -1),
+    (dict(sinks=129), -2),
+    (dict(H=6, Hkv=4), -1),
+    (dict(H=5, Hkv=5, paired=1), -1),
+    (dict(H=6, Hkv=3, paired=1), -1),
+    (dict(hd=96), -2),
+    (dict(dtype=1, hd=160), -2),
+    (dict(dtype=1, hd=96), -3),
+    (dict(dtype=7), -1),
+    (dict(batch=0), -1),
+    (dict(total=-1), -1),
+    (dict(paired=2), -1),
+    (dict(scale=float("nan")), -1),
+    (dict(q=MIS), -1),
+    (dict(v=None), -1),
+    (dict(lse=A + 2), -1),
+    (dict(cu=None), -1),
+])
+def test_sinks_argument_errors(pha, bwd, kw, code):
+    assert _sinks(pha, bwd, **kw) == code
+
+
+def test_sinks_backward_needs_the_forwards_outputs(pha):
+    for kw in (dict(lse=None), dict(o=None), dict(dout=None), dict(dq=None), dict(dk=MIS)):
+        assert _sinks(pha, True, **kw) == -1
+    assert _sinks(pha, True, total=0, q=None, k=None, v=None, o=None, lse=None, dout=None, dq=None,
+                  dk=None, dv=None, ws=None) == 0      # nothing to do
+
+
+def _paged(pha, **kw):
+    a = dict(q=A, k=A, v=A, table=A, max_pages=8, n_pages=64, page=16, cu=A, lens=A, batch=2, max_q=4,
+             max_kv=100, total=8, H=4, Hkv=4, hd=64, dtype=0, window=0, sinks=0, paired=0, scale=0.0,
+             o=A, lse=A, ws=A, bytes=10, status=A)
+    a.update(kw)
+    return pha.library().pha_attn_paged_fwd(
+        a["q"], a["k"], a["v"], a["table"], a["max_pages"], a["n_pages"], a["page"], a["cu"],
+        a["lens"], a["batch"], a["max_q"], a["max_kv"], a["total"], a["H"], a["Hkv"], a["hd"],
+        a["dtype"], a["window"], a["sinks"], a["paired"], ctypes.c_float(a["scale"]), a["o"],
+        a["lse"], a["ws"], a["bytes"], a["status"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, -3),
+    (dict(page=1), -3),
+    (dict(page=24), -1),                       # no power of two
+    (dict(page=0), -1),
+    (dict(n_pages=0), -1),
+    (dict(max_pages=0), -1),
+    (dict(n_pages=1 << 27, page=16), -1),      # more rows than 31 bits count
+    (dict(sinks=-1), -1),
+    (dict(sinks=1000, window=5), -3),
+    (dict(hd=96), -2),
+    (dict(dtype=1, hd=129), -2),
+    (dict(dtype=3), -1),
+    (dict(H=6, Hkv=4), -1),
+    (dict(H=3, Hkv=3, paired=1), -1),
+    (dict(max_q=-1), -1),
+    (dict(batch=0), -1),
+    (dict(scale=float("nan")), -1),
+    (dict(q=None), -1),
+    (dict(k=MIS), -1),
+    (dict(table=None), -1),
+    (dict(table=A + 2), -1),
+    (dict(cu=None), -1),
+    (dict(lens=None), -1),
+    (dict(status=A + 1), -1),
+    (dict(ws=None, bytes=1 << 30), -3),
+    (dict(total=0, q=None, o=None, lse=None, ws=None), 0),
+])
+def test_paged_argument_errors(pha, kw, code):
+    assert _paged(pha, **kw) == code
+
+
+def test_paged_workspace_bytes(pha):
+    import torch
+
+    size = lambda **kw: pha.pha_attn_paged_workspace_bytes(**{**dict(
+        batch=4, max_q=1, max_kv=500, total_q=4, n_heads=8, n_kv_heads=2, head_dim=64,
+        dtype=torch.bfloat16), **kw})
+    assert size() >= 256
+    assert size(batch=0) == 0 and size(n_heads=7) == 0 and size(max_kv=-1) == 0
+    assert size(max_kv=1 << 20) >= size()
+    # a window bounds what splits can be worth
+    assert size(max_kv=1 << 20, window=64) <= size(max_kv=1 << 20)
+
+
+def _append(pha, **kw):
+    a = dict(k=A, v=A, kp=A, vp=A, table=A, max_pages=8, n_pages=64, page=16, cu=A, lens=A, batch=2,
+             total=8, Hkv=4, hd=64, esize=2, status=A)
+    a.update(kw)
+    return pha.library().pha_cache_append(
+        a["k"], a["v"], a["kp"], a["vp"], a["table"], a["max_pages"], a["n_pages"], a["page"],
+        a["cu"], a["lens"], a["batch"], a["total"], a["Hkv"], a["hd"], a["esize"], a["status"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(total=0), 0),
+    (dict(total=-1), -1),
+    (dict(page=12), -1),
+    (dict(esize=8), -1),
+    (dict(Hkv=1, hd=4), -1),                   # rows of 8 bytes
+    (dict(k=MIS), -1),
+    (dict(vp=None), -1),
+    (dict(table=None), -1),
+    (dict(lens=A + 2), -1),
+    (dict(status=A + 2), -1),
+])
+def test_append_argument_errors(pha, kw, code):
+    assert _append(pha, **kw) == code
+
+
+def test_cache_call_argument_errors(pha):
+    lib = pha.library()
+    big = pha.pha_cache_workspace_bytes(64, 4)
+    assert pha.pha_cache_workspace_bytes(0, 4) == 0 and pha.pha_cache_workspace_bytes(4, 0) == 0
+
+    def fork(table=A, lens=A, refs=A, src=A, dst=A, n=2, ws=A, size=big, pages=64, status=None):
+        return lib.pha_cache_fork(table, 8, lens, 4, refs, pages, src, dst, n, ws, size, status, None)
+
+    assert fork(size=big - 1) == -3 and fork(ws=None) == -3 and fork(ws=MIS) == -3
+    for kw in (dict(table=None), dict(lens=None), dict(refs=A + 1), dict(src=None), dict(dst=A + 2),
+               dict(n=-1), dict(n=5), dict(pages=0), dict(status=A + 3)):
+        assert fork(**kw) == -1, kw
+
+    def reserve(page=16, seqs=A, new=A, k=A, v=A, layers=1, nbytes=4096, ws=None):
+        return lib.pha_cache_reserve(A, 8, A, 4, A, 64, page, seqs, new, 2, k, v, layers, nbytes, ws,
+                                     big, None, None)
+
+    assert reserve() == -3
+    for kw in (dict(page=10), dict(seqs=None), dict(new=A + 2), dict(k=None), dict(v=MIS),
+               dict(layers=0), dict(nbytes=24), dict(nbytes=0)):
+        assert reserve(**kw) == -1, kw
+
+    def free(seqs=A, ws=None):
+        return lib.pha_cache_free(A, 8, A, 4, A, 64, seqs, 2, ws, big, None, None)
+
+    assert free() == -3 and free(seqs=None) == -1
+
+    def trim(window=5, sinks=0, page=16, paired=0):
+        return lib.pha_cache_trim(A, 8, None, 4, A, 64, page, window, sinks, paired, None, None)
+
+    assert trim() == -1                        # lengths are needed
+    for kw in (dict(window=0), dict(sinks=-1), dict(page=3), dict(paired=2)):
+        assert trim(**kw) == -1
+
+    def compact(k=A, layers=1, nbytes=4096, ws=None):
+        return lib.pha_cache_compact(A, 8, 4, A, 64, k, A, layers, nbytes, ws, big, None, None)
+
+    assert compact() == -3
+    assert compact(k=None) == -1 and compact(layers=0) == -1 and compact(nbytes=8) == -1
+
+
+def test_binding_checks_tensors(pha):
+    """The binding refuses what the library cannot see, before the library is called."""
+    import torch
+
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(1 << 12, dtype=torch.uint8)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    kw = dict(window=2, sinks=1)
+    with pytest.raises(ValueError, match="CUDA"):
+        pha.pha_attn_sinks_fwd(q, q, q, cu, 4, q, None, ws, **kw)
+    with pytest.raises(ValueError, match="contiguous"):
+        pha.pha_attn_sinks_fwd(torch.zeros(2, 4, 64, dtype=torch.bfloat16).transpose(0, 1), q, q, cu, 4,
+                               q, None, ws, **kw)
+    with pytest.raises(TypeError):
+        pha.pha_attn_sinks_fwd(q.to(torch.float16), q, q, cu, 4, q, None, ws, **kw)
+    with pytest.raises(TypeError, match="o:"):
+        pha.pha_attn_sinks_fwd(q, q, q, cu, 4, q.float(), None, ws, **kw)
+    i32 = dict(dtype=torch.int32)
+    with pytest.raises(TypeError, match="page_table"):
+        pha.pha_cache_trim(torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, **i32),
+                           torch.zeros(9, **i32), 16, window=4)
