@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
                                                                    const float* __restrict__ dsum,
                                                                    T* __restrict__ dq) {
     constexpr int NC = HP / (4 * kLanesPerRow);
+    if (p.checked && p.checked->status != DEV_OK) return;
     extern __shared__ float4 bsm4[];
     float* ks = reinterpret_cast<float*>(bsm4);  // [kStage][HP]
     float* vs = ks + kStage * HP;                // [kStage][HP]
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
                                                                      T* __restrict__ dk,
                                                                      T* __restrict__ dv) {
     constexpr int NC = HP / (4 * kLanesPerRow);
+    if (p.checked && p.checked->status != DEV_OK) return;
     extern __shared__ float4 bsm4[];
     float* qs = reinterpret_cast<float*>(bsm4);  // [kStage][HP]
     float* gs = qs + kStage * HP;                // [kStage][HP]

@@ -26,8 +26,8 @@ struct WorkspaceHeader {
     int n_items;
     int status;
     uint32_t magic;     // kScheduleMagic while the fields below describe a valid list
-    int key[10];        // mode, batch, max_len, total_tokens, slot_mult, heads, causal, window,
-                        // capacity, n_buckets
+    int key[10];        // mode | sinks << 8, batch, max_len, total_tokens, slot_mult, heads, causal,
+                        // window, capacity, n_buckets
     uint32_t checksum;  // of the items, in order
     int reused;         // 1 when the last scheduler call kept the list (read by tests)
 };
@@ -51,6 +51,12 @@ inline size_t workspace_doc_bytes(int batch) {
 // Work-list shapes of the scheduler: block items (attn_tc), band items (attn_band and the band
 // backward), and tile items ordered by the number of key tiles a query tile sees (dQ) or of query
 // tiles that see a key tile (dK / dV).
+//
+// Sinks (AttnProblem::sinks > 0, at most kBlockN, with a window): the first key tile of a document is
+// seen by every later query tile. Its K-list item takes the query tiles that see it by the window; the
+// query tiles behind ("far", only the sinks see them) are cut into pieces of sink_piece_tiles, each
+// an item of its own so that no CTA walks a whole document: item field "query tiles" is 1 for an
+// ordinary tile and 2 + piece for a piece.
 enum ScheduleMode : int { kSchedBlock = 0, kSchedBand = 1, kSchedTilesQ = 2, kSchedTilesK = 3 };
 
 struct AttnProblem {
@@ -69,6 +75,9 @@ struct AttnProblem {
     int window;
     int sinks;            // first slots of a document that every later query sees (backward only;
                           // 0: none)
+    // float32 dk, dv of the sinks by far pieces: [sink_part_slots()][kv_heads][sinks][2][head_dim]
+    float* sink_part;
+    const WorkspaceHeader* checked;  // CUDA-core backward with sinks: do nothing unless its status is ok
     float scale;
     void* o;
     float* lse;
@@ -84,6 +93,30 @@ struct AttnProblem {
     float qk_scale;
     float v_scale;
 };
+
+// Query tiles of a far piece: about as many as an ordinary key tile's item has, and few enough pieces
+// for their number to fit the item word.
+__host__ __device__ inline int sink_piece_tiles(int window, int max_len, int slot_mult) {
+    const int by_window = (window + kBlockN - 1) / kBlockN;
+    const int64_t tiles = static_cast<int64_t>(max_len) * slot_mult / kBlockN + 1;
+    const int by_count = static_cast<int>(tiles / 32000) + 1;
+    const int c = by_window > 8 ? by_window : 8;
+    return c > by_count ? c : by_count;
+}
+
+// Slots of sink_part: one per document (the window's part), then the far pieces, piece f of document
+// d at batch + d + (its first query slot) / (piece slots). Pieces of a document start exactly one
+// piece apart and documents do not overlap, so the places are distinct.
+__host__ __device__ inline int64_t sink_part_slots(int batch, int64_t total_slots, int piece_tiles) {
+    return 2 * static_cast<int64_t>(batch) + total_slots / (static_cast<int64_t>(piece_tiles) * kBlockN) + 1;
+}
+
+// First far query tile of a document of `slots` slots (its number of tiles when there is none).
+__host__ __device__ inline int sink_far_tile(int window, int64_t slots) {
+    const int64_t last = slots - 1;
+    const int64_t q_last = (last < kBlockN - 1 ? last : kBlockN - 1) + window - 1;  // sees key tile 0
+    return static_cast<int>((q_last < last ? q_last : last) / kBlockN) + 1;
+}
 
 cudaError_t launch_rope_tables(float* cos_tab, float* sin_tab, int rows, int head_dim, int paired,
                                double base, cudaStream_t stream);
@@ -144,7 +177,12 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
                                const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
                                const CUtensorMap& tm_dk, const CUtensorMap& tm_dv,
                                const float* dsum, void* dq, void* dk, void* dv, const int4* items,
-                               WorkspaceHeader* hdr, int which, cudaStream_t stream);
+                               WorkspaceHeader* hdr, int which, cudaStream_t stream,
+                               bool sinks = false);
+
+// Sum of the sinks' dk, dv over the far pieces of each document (p.sink_part), into dk, dv (bf16).
+cudaError_t launch_attn_bwd_sink_sum(const AttnProblem& p, void* dk, void* dv,
+                                     const WorkspaceHeader* hdr, cudaStream_t stream);
 
 // RoPE preceded by the QK RMS-norm of every head row (weights may be NULL = ones).
 cudaError_t launch_qk_norm_rope(void* q, void* k, const float* q_weight, const float* k_weight,

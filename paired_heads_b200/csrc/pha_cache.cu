@@ -205,6 +205,7 @@ struct PagedPlan {
     bool gather;                 // the tensor-core kernel with a work list
     int n_splits, split_keys;
     int pack, tile_tokens;
+    int window, sinks;           // as the kernels take them
     int64_t items;
     size_t before, list, part_o, part_lse, bytes;  // workspace offsets
 };
@@ -217,15 +218,19 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
         n_heads % n_kv_heads != 0 || head_dim <= 0 || head_dim > 128 || sinks < 0 ||
         (paired != 0 && paired != 1) || (paired && ((n_heads & 1) || (n_kv_heads & 1))))
         return false;
+    w = PagedPlan{};
     const int mult = paired ? 2 : 1;
     const int heads = n_heads / mult, kv_heads = n_kv_heads / mult;
     // the most key columns the new tokens of one sequence can see
     int64_t most = static_cast<int64_t>(max_kv) * mult;
+    w.window = window > 0 && window < most ? window : 0;  // a window past every cache hides nothing
+    w.sinks = sinks < most ? sinks : static_cast<int>(most);
+    window = w.window;
+    sinks = w.sinks;
     if (window > 0) {
         const int64_t seen = static_cast<int64_t>(window) + static_cast<int64_t>(max_q) * mult + sinks;
         most = seen < most ? seen : most;
     }
-    w = PagedPlan{};
     w.gather = dtype == PHA_BF16;
     if (w.gather) {
         w.pack = gather_pack(heads, kv_heads);
@@ -313,8 +318,8 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
     p.heads = n_heads / p.mult;
     p.kv_heads = n_kv_heads / p.mult;
     p.head_dim = head_dim;
-    p.window = window > 0 ? window : 0;
-    p.sinks = sinks;
+    p.window = w.window;
+    p.sinks = w.sinks;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     p.n_splits = w.n_splits;
     p.split_keys = w.split_keys;

@@ -7,6 +7,7 @@
 #include "../../include/pha_sinks.h"
 #include "gather.cuh"
 #include "kernels.cuh"
+#include "tensor_map.cuh"
 
 using namespace pha;
 
@@ -29,6 +30,12 @@ pha_status shape_status(int batch, int max_len, int total_tokens, int n_heads, i
     return PHA_OK;
 }
 
+// A window that reaches past the longest document hides nothing: no window (0), as the kernels' index
+// arithmetic wants it.
+int real_window(int window, int max_len, int paired) {
+    return window > 0 && window < static_cast<int64_t>(max_len) * (paired ? 2 : 1) ? window : 0;
+}
+
 size_t padded(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Work items of the forward (documents of any lengths up to max_len).
@@ -36,7 +43,35 @@ int64_t fwd_items(int batch, int max_len, int n_heads, int n_kv_heads, int windo
     const int mult = paired ? 2 : 1, heads = n_heads / mult;
     const int pack = gather_pack(heads, n_kv_heads / mult);
     const int64_t slots = static_cast<int64_t>(max_len) * mult;
+    window = real_window(window, max_len, paired);
     return gather_items(batch, slots, slots * batch, gather_tile_tokens(pack, window, sinks), heads / pack, 1);
+}
+
+// Backward: header, per-document scratch and the largest work list (key tiles and far pieces), then
+// D, then the far pieces' partial sums.
+struct BwdPlan {
+    int64_t items;
+    size_t list, dsum, part, bytes;
+};
+
+BwdPlan bwd_plan(int batch, int max_len, int total_tokens, int n_heads, int n_kv_heads, int head_dim,
+                 int window, int sinks, int paired) {
+    const int mult = paired ? 2 : 1;
+    const int64_t tiles = (static_cast<int64_t>(max_len) * mult + kBlockN - 1) / kBlockN;
+    window = real_window(window, max_len, paired);
+    const bool far = window > 0 && sinks > 0;
+    const int piece = far ? sink_piece_tiles(window, max_len, mult) : 1;
+    const int64_t pieces = far ? (tiles + piece - 1) / piece : 0;
+    BwdPlan w{};
+    w.items = static_cast<int64_t>(batch) * (tiles + pieces) * (n_heads / mult);
+    w.list = kWorkspaceHeaderBytes + workspace_doc_bytes(batch);
+    w.dsum = w.list + padded(sizeof(int4) * static_cast<size_t>(w.items));
+    w.part = w.dsum + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
+    const int64_t slots = static_cast<int64_t>(total_tokens) * mult;
+    w.bytes = w.part + (far ? padded(sizeof(float) * static_cast<size_t>(sink_part_slots(batch, slots, piece)) *
+                                     (n_kv_heads / mult) * sinks * 2 * head_dim)
+                            : 0);
+    return w;
 }
 
 }  // namespace
@@ -54,11 +89,10 @@ size_t pha_attn_sinks_workspace_bytes(int batch, int max_len, int n_heads, int n
 size_t pha_attn_sinks_bwd_workspace_bytes(int batch, int max_len, int total_tokens, int n_heads,
                                           int n_kv_heads, int head_dim, int window, int sinks,
                                           int paired) {
-    (void)window;
     if (shape_status(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, PHA_F32, sinks, paired,
                      0.f) != PHA_OK)
         return 0;
-    return pha_attn_bwd_workspace_bytes(batch, max_len, total_tokens, n_heads, head_dim, paired);
+    return bwd_plan(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, window, sinks, paired).bytes;
 }
 
 pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
@@ -92,7 +126,7 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
     p.heads = n_heads / p.mult;
     p.kv_heads = n_kv_heads / p.mult;
     p.head_dim = head_dim;
-    p.window = window > 0 ? window : 0;
+    p.window = real_window(window, max_len, paired);
     p.sinks = sinks;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     p.n_splits = 1;
@@ -144,15 +178,41 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
     p.kv_heads = n_kv_heads / p.slot_mult;
     p.head_dim = head_dim;
     p.causal = 1;
-    p.window = window > 0 ? window : 0;
+    p.window = real_window(window, max_len, paired);
     p.sinks = p.window > 0 ? sinks : 0;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     p.lse = const_cast<float*>(lse);
+    const BwdPlan w = bwd_plan(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, window, sinks, paired);
     auto* base = static_cast<uint8_t*>(workspace);
-    float* dsum = reinterpret_cast<float*>(base + kWorkspaceHeaderBytes);
-    if (launch_attn_bwd_dsum(p, o, dout, dsum, dtype == PHA_BF16, stream) != cudaSuccess)
+    auto* hdr = reinterpret_cast<WorkspaceHeader*>(base);
+    auto* docs = reinterpret_cast<int*>(base + kWorkspaceHeaderBytes);
+    auto* items = reinterpret_cast<int4*>(base + w.list);
+    float* dsum = reinterpret_cast<float*>(base + w.dsum);
+    p.sink_part = reinterpret_cast<float*>(base + w.part);
+    p.checked = hdr;
+    const int capacity = w.items < INT32_MAX ? static_cast<int>(w.items) : INT32_MAX;
+    const bool tc = dtype == PHA_BF16;
+    // the scheduler also checks cu_seqlens; without a list to walk (CUDA cores) only that is used
+    if (launch_schedule(p, kSchedTilesQ, capacity, docs, items, hdr, stream) != cudaSuccess ||
+        launch_attn_bwd_dsum(p, o, dout, dsum, tc, stream) != cudaSuccess)
         return PHA_ERR_CUDA;
-    return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, dtype == PHA_BF16, stream));
+    if (!tc) return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, 0, stream));
+    const uint64_t rows = static_cast<uint64_t>(total_tokens) * p.slot_mult;
+    const uint64_t wq = static_cast<uint64_t>(p.heads) * head_dim, wk = static_cast<uint64_t>(p.kv_heads) * head_dim;
+    CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
+    if (!encode_slot_map(&tq, q, wq, rows) || !encode_slot_map(&tk, k, wk, rows) ||
+        !encode_slot_map(&tv, v, wk, rows) || !encode_slot_map(&tdo, dout, wq, rows) ||
+        !encode_slot_map(&tdq, dq, wq, rows, 32) || !encode_slot_map(&tdk, dk, wk, rows, 16) ||
+        !encode_slot_map(&tdv, dv, wk, rows, 16))
+        return PHA_ERR_CUDA;
+    if (launch_attn_bwd_zero_outside(p, dq, dk, dv, stream) != cudaSuccess ||
+        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, items, hdr, 1, stream, true) !=
+            cudaSuccess ||
+        launch_schedule(p, kSchedTilesK, capacity, docs, items, hdr, stream) != cudaSuccess ||
+        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, items, hdr, 2, stream, true) !=
+            cudaSuccess)
+        return PHA_ERR_CUDA;
+    return p.sinks > 0 ? of(launch_attn_bwd_sink_sum(p, dk, dv, hdr, stream)) : PHA_OK;
 }
 
 }  // extern "C"

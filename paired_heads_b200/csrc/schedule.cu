@@ -106,6 +106,14 @@ __device__ __forceinline__ int mode_rows(int mode) {
     return mode == kSchedBlock ? kItemRows : (mode == kSchedBand ? kBandRows : kBlockM);
 }
 
+// K lists with sinks: the pieces of a document's far query tiles.
+__device__ __forceinline__ int64_t far_pieces(const AttnProblem& p, int64_t slots, int mode) {
+    if (mode != kSchedTilesK || p.sinks == 0 || p.window <= 0 || slots == 0) return 0;
+    const int64_t far = (slots + kBlockN - 1) / kBlockN - sink_far_tile(p.window, slots);
+    const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
+    return (far + c - 1) / c;
+}
+
 __device__ __forceinline__ BlockRange block_range(const AttnProblem& p, int64_t a, int64_t b,
                                                   int blk, int n_buckets, int mode) {
     BlockRange r;
@@ -117,6 +125,15 @@ __device__ __forceinline__ BlockRange block_range(const AttnProblem& p, int64_t 
         // tile j = blk of the document's 128-slot tiles
         const int64_t last = (b - a - 1) / kBlockN;  // index of the document's last tile
         int64_t lo = 0, hi = last;
+        if (blk > last) {  // a far piece of the first key tile (sinks)
+            const int piece = static_cast<int>(blk - last - 1);
+            const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
+            const int64_t first = sink_far_tile(p.window, b - a) + static_cast<int64_t>(piece) * c;
+            cost = last - first + 1 < c ? last - first + 1 : c;
+            r.item = make_int4(static_cast<int>(a), 2 + piece, static_cast<int>(b), static_cast<int>(a));
+            r.cost = static_cast<int>(cost >= n_buckets ? n_buckets - 1 : cost);
+            return r;
+        }
         if (mode == kSchedTilesQ) {  // key tiles this query tile sees
             if (p.causal) {
                 hi = blk;
@@ -130,7 +147,7 @@ __device__ __forceinline__ BlockRange block_range(const AttnProblem& p, int64_t 
                 hi = ((q_last < b ? q_last : b - 1) - a) / kBlockN;
             }
         }
-        cost = hi - lo + 1;
+        cost = hi - lo + 1 + (mode == kSchedTilesQ && p.sinks > 0 && lo > 0 ? 1 : 0);
         r.item = make_int4(static_cast<int>(q0), ((blk > 0 ? 1 : 0) << 15) | 1, static_cast<int>(b),
                            static_cast<int>(a));
     } else if (mode == kSchedBand) {
@@ -168,7 +185,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnProblem p, 
     const int tid = threadIdx.x;
     const int64_t mult = p.slot_mult;
     const int rows = mode_rows(mode);
-    const int key[10] = {mode, p.batch, p.max_len, p.total_tokens, p.slot_mult, p.heads,
+    const int key[10] = {mode | (p.sinks << 8), p.batch, p.max_len, p.total_tokens, p.slot_mult, p.heads,
                          p.causal, p.window, capacity, n_buckets};
 
     // (0) the list of an earlier call with the same inputs is kept
@@ -205,7 +222,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnProblem p, 
         if (a0 < 0 || b0 < a0 || b0 > p.total_tokens || b0 - a0 > p.max_len)
             atomicOr(&bad, 1);
         else
-            nb = static_cast<int>(((b0 - a0) * mult + rows - 1) / rows);
+            nb = static_cast<int>(((b0 - a0) * mult + rows - 1) / rows + far_pieces(p, (b0 - a0) * mult, mode));
         doc_blocks[d] = nb;
     }
     __syncthreads();

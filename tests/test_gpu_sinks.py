@@ -108,6 +108,9 @@ CASES = [
     ((500,), 2, 1, 64, BF16, 5000, 7, False),            # a window past the document
     ((384,), 34, 2, 64, BF16, 90, 10, False),            # groups of 17
     ((260,), 256, 1, 64, BF16, 70, 2, False),            # one kv head for 256
+    ((4100, 1500), 2, 2, 64, BF16, 60, 4, False),        # sinks that many far queries see
+    ((3000,), 4, 1, 128, BF16, 200, 100, False),
+    ((2600,), 2, 2, 128, BF16, 1100, 9, True),
     ((64, 1, 37, 130), 4, 2, 16, F32, 9, 3, False),
     ((150, 20), 4, 4, 96, F32, 17, 33, True),
     ((90,), 2, 1, 5, F32, 8, 2, False),                  # an odd head_dim
