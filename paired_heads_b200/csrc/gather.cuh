@@ -33,28 +33,33 @@ struct GatherProblem {
     int heads, kv_heads, head_dim;      // of the slot view
     int window, sinks;
     float scale;
-    // Split key ranges: partial results [split][q slot][head], normalised o (float32) and log2 of
-    // the sum of exponentials; split_keys > 0: split s has columns [s, s + 1) * split_keys of its
-    // sequence (single tokens), and a sequence with one split writes o itself.
+    // Partial results: normalised o (float32) and log2 of the sum of exponentials. CUDA cores and single
+    // tokens: [split][q slot][head], split s having columns [s, s + 1) * split_keys of its sequence
+    // (a sequence with one split writes o itself). Tensor cores: [2 per CTA][row of the tile].
     int n_splits, split_keys;
     float* part_o;
     float* part_lse;
     int32_t* status;         // may be NULL
-    // Work list (gather_plan.cu): its header, which also holds the device status of a call with one
-    // (NULL: none), and the items.
+    // Plan of the tensor-core kernel (gather_plan.cu): its header, which also holds the device status
+    // of a call with one (NULL: none), the row tiles and where each CTA's share begins.
     WorkspaceHeader* hdr;
-    int4* items;
+    int4* tiles;
+    int4* starts;
+    int n_cta;               // CTAs that share the work
     // Tensor cores: a row of a query tile is (token, head) with `pack` heads of one kv head's group
-    // side by side (rows r = token * pack + head), tile_tokens tokens a work item.
+    // side by side (rows r = token * pack + head), tile_tokens tokens a row tile.
     int pack, tile_tokens;
+    int box_rows;            // rows of a TMA box over k / v; paged: they lie in one page, and columns
+                             // begin at multiples of it (1: no TMA)
 };
 
-constexpr int kGatherRows = 2 * kBlockM;  // rows of a work item (two sub-tiles)
-
-// Work item, two int4:
-//   x0 = first q slot, y0 = (pack chunk << 16) | tokens, z0 = position of the first token,
-//   w0 = sequence (paged) or slot of key 0 (documents);
-//   x1 = first key tile, y1 = past the last key tile (of this split), z1 = split.
+// One row tile: up to 256 rows (two sub-tiles) of one sequence, times each chunk of `pack` heads.
+//   x = first q slot, y = tokens | keys of the sequence behind the tile's last (at most 127) << 16,
+//   z = position of the first token, w = sequence (paged) or slot of key 0 (documents).
+// The work of all (row tile, chunk) items lies on one line, key tile by key tile with one step more
+// per item for its fixed costs, and is cut into n_cta equal shares: starts[c] = (row tile, chunk, key
+// tile) where CTA c begins. Items that a cut divides leave partial rows, which attn_join_cuts joins.
+constexpr int kGatherRows = 2 * kBlockM;
 
 struct GatherSeq {
     int64_t q0;    // first q slot
@@ -88,9 +93,10 @@ struct GatherCols {
     int total;   // all columns
 };
 
-__device__ __forceinline__ GatherCols gather_cols(const GatherProblem& p, int p0, int n) {
+// align (a power of two): lo is rounded down to a multiple of it.
+__device__ __forceinline__ GatherCols gather_cols(const GatherProblem& p, int p0, int n, int align = 1) {
     GatherCols c;
-    c.lo = (p.window > 0 && p0 - p.window + 1 > 0) ? p0 - p.window + 1 : 0;
+    c.lo = (p.window > 0 && p0 - p.window + 1 > 0) ? (p0 - p.window + 1) & ~(align - 1) : 0;
     c.n_w = p0 + n - c.lo;
     c.total = c.n_w + (p.sinks < c.lo ? p.sinks : c.lo);
     return c;
@@ -135,32 +141,59 @@ inline int gather_pack(int heads, int kv_heads) {
     return g <= kBlockM ? g : 1;
 }
 
-// Tokens of a work item: as many as fit its rows, or fewer where that saves a whole key tile and the
+// Columns of a tile's first key are aligned to this (see box_rows).
+__host__ __device__ inline int gather_align(bool paged, int box_rows) { return paged ? box_rows : 1; }
+
+// Tokens of a row tile: as many as fit its rows, or fewer where that saves a whole key tile and the
 // rows per key tile go up. (A run of T tokens sees window + T - 1 + sinks columns, so with a window
 // of a multiple of 128 the last tile would hold a few columns only.)
-inline int gather_tile_tokens(int pack, int window, int sinks) {
+inline int gather_tile_tokens(int pack, int window, int sinks, int align) {
     const int most = kGatherRows / pack;
     if (window <= 0) return most;
-    const int64_t cols = static_cast<int64_t>(window) + most - 1 + sinks;
-    const int64_t tiles = (cols + kBlockN - 1) / kBlockN;
-    const int64_t fewer = (tiles - 1) * kBlockN - window - sinks + 1;
-    return fewer >= 1 && tiles > 1 && fewer * tiles > most * (tiles - 1) ? static_cast<int>(fewer) : most;
+    const int64_t fixed = static_cast<int64_t>(window) - 1 + (align - 1) + sinks;
+    const int64_t tiles = (fixed + most + kBlockN - 1) / kBlockN;
+    const int64_t fewer = (tiles - 1) * kBlockN - fixed;
+    return fewer >= 1 && fewer * tiles > most * (tiles - 1) ? static_cast<int>(fewer) : most;
 }
 
-// Bound on the work items of a call (n_splits of each row tile).
-inline int64_t gather_items(int batch, int64_t max_q, int64_t total_q, int tile_tokens, int chunks, int n_splits) {
+// Bound on the row tiles of a call.
+inline int64_t gather_tiles(int batch, int64_t max_q, int64_t total_q, int tile_tokens) {
     const int64_t per_seq = (max_q + tile_tokens - 1) / tile_tokens;
     const int64_t by_rows = total_q / tile_tokens + batch;
-    return (per_seq * batch < by_rows ? per_seq * batch : by_rows) * chunks * n_splits;
+    return per_seq * batch < by_rows ? per_seq * batch : by_rows;
 }
 
-// Checks the lengths and writes the work list (p.items NULL: the check alone). strict: any bad length makes the list empty (header
-// status 1); otherwise only the bad sequences are left out (p.status 1). before: int[batch + 1].
-cudaError_t launch_gather_plan(const GatherProblem& p, int64_t capacity, int* before, bool strict,
-                               cudaStream_t stream);
+constexpr int kGatherCtas = 148;      // SMs of a B200; workspaces may not depend on the device at hand
+constexpr int kGatherMinSteps = 3;    // key tiles (and item costs) of a CTA's share, at least
 
-// bf16, head_dim 64 / 128, on the tensor cores, over the work list. max_items bounds the grid.
-cudaError_t launch_attn_gather(const GatherProblem& p, int64_t max_items, cudaStream_t stream);
+// Workspace of the plan and the partial rows, from byte 0 (the header).
+struct GatherSpace {
+    size_t before, steps, tiles, starts, part_o, part_lse, bytes;
+};
+inline GatherSpace gather_space(int batch, int64_t tiles, int head_dim) {
+    const auto padded = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
+    GatherSpace w;
+    w.before = kWorkspaceHeaderBytes;
+    w.steps = w.before + padded(sizeof(int) * (static_cast<size_t>(batch) + 1));
+    w.tiles = w.steps + padded(sizeof(int64_t) * (static_cast<size_t>(tiles) + 1));
+    w.starts = w.tiles + padded(sizeof(int4) * static_cast<size_t>(tiles));
+    w.part_o = w.starts + padded(sizeof(int4) * (kGatherCtas + 1));
+    const size_t rows = 2 * static_cast<size_t>(kGatherCtas) * kGatherRows;
+    w.part_lse = w.part_o + rows * head_dim * sizeof(float);
+    w.bytes = w.part_lse + rows * sizeof(float);
+    return w;
+}
+
+// Checks the lengths and lays out the work (max_tiles 0: the check alone). strict: any bad length
+// makes the plan empty (header status 1); otherwise only the bad sequences are left out (p.status 1).
+// before: int[batch + 1], steps: int64[max_tiles + 1].
+cudaError_t launch_gather_plan(const GatherProblem& p, int64_t max_tiles, int* before, int64_t* steps,
+                               bool strict, cudaStream_t stream);
+
+// bf16, head_dim 64 / 128, on the tensor cores, by the plan; then the cut items. tm_q: encode_pack_map
+// over q (used when pack divides 128); tm_k, tm_v: maps over the rows of k / v, 64 x box_rows boxes.
+cudaError_t launch_attn_gather(const GatherProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                               const CUtensorMap& tm_v, cudaStream_t stream);
 
 // float32 on CUDA cores: one warp per (row, split).
 cudaError_t launch_attn_rows(const GatherProblem& p, cudaStream_t stream);

@@ -8,6 +8,7 @@
 #include "cache.cuh"
 #include "gather.cuh"
 #include "kernels.cuh"
+#include "tensor_map.cuh"
 
 using namespace pha;
 
@@ -198,21 +199,21 @@ pha_status pha_cache_compact(int32_t* page_table, int max_pages, int n_seqs, int
 namespace {
 
 constexpr int kRowsSplitKeys = 1024;  // key columns of one warp's split (float32)
-constexpr int kGpuSms = 148;          // workspaces may not depend on the device at hand
-constexpr int kMinSplitTiles = 4;     // key tiles of a split of the tensor-core kernel, at least
 
 struct PagedPlan {
-    bool gather;                 // the tensor-core kernel with a work list
-    int n_splits, split_keys;
-    int pack, tile_tokens;
+    bool gather;                 // the tensor-core kernel with a plan
     int window, sinks;           // as the kernels take them
-    int64_t items;
-    size_t before, list, part_o, part_lse, bytes;  // workspace offsets
+    int n_splits, split_keys;
+    int pack, tile_tokens, box_rows;
+    int64_t tiles;
+    GatherSpace space;
+    size_t part_o, part_lse, bytes;  // workspace offsets
 };
 
 // The path, the splits and the workspace of a paged call. false: arguments out of range.
 bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int n_heads,
-                int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks, int paired) {
+                int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks, int paired,
+                int page_size = 0) {
     if (batch <= 0 || max_q < 0 || max_kv < 0 || total_q < 0 || total_q > (1 << 28) ||
         max_kv > (1 << 29) || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
         n_heads % n_kv_heads != 0 || head_dim <= 0 || head_dim > 128 || sinks < 0 ||
@@ -233,27 +234,29 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
     }
     w.gather = dtype == PHA_BF16;
     if (w.gather) {
+        // A TMA box stays in one page. Without a window columns begin at position 0 and it may be a whole
+        // tile; with one they begin at a multiple of the box, so it is kept to 32 rows (16 of the
+        // first tile's columns wasted on average).
+        const int most_rows = window > 0 ? 32 : kBlockN;
+        const int page_slots = page_size * mult;
+        w.box_rows = page_slots < most_rows ? page_slots : most_rows;
+        if (w.box_rows < 8) w.box_rows = 1;  // below the 8 rows of a swizzle pattern: gathered row by row
         w.pack = gather_pack(heads, kv_heads);
-        w.tile_tokens = gather_tile_tokens(w.pack, window, sinks);
-        const int64_t base = gather_items(batch, static_cast<int64_t>(max_q) * mult,
-                                          static_cast<int64_t>(total_q) * mult, w.tile_tokens, heads / w.pack, 1);
-        // few row tiles: split their key tiles so that every SM has an item
-        const int64_t tiles = (most + kBlockN - 1) / kBlockN;
-        int64_t s = base > 0 ? kGpuSms / base : 1;
-        if (s > tiles / kMinSplitTiles) s = tiles / kMinSplitTiles;
-        w.n_splits = s < 1 ? 1 : static_cast<int>(s);
-        w.items = base * w.n_splits;
-        if (w.items > INT32_MAX) return false;
-    } else {
-        w.split_keys = kRowsSplitKeys;
-        w.n_splits = static_cast<int>((most + w.split_keys - 1) / w.split_keys);
-        if (w.n_splits < 1) w.n_splits = 1;
+        w.tile_tokens = gather_tile_tokens(w.pack, window, sinks, most_rows);
+        w.tiles = gather_tiles(batch, static_cast<int64_t>(max_q) * mult, static_cast<int64_t>(total_q) * mult,
+                               w.tile_tokens);
+        w.space = gather_space(batch, w.tiles, head_dim);
+        w.part_o = w.space.part_o;
+        w.part_lse = w.space.part_lse;
+        w.bytes = w.space.bytes;
+        return true;
     }
+    w.split_keys = kRowsSplitKeys;
+    w.n_splits = static_cast<int>((most + w.split_keys - 1) / w.split_keys);
+    if (w.n_splits < 1) w.n_splits = 1;
     const size_t rows = static_cast<size_t>(total_q) * n_heads;
     const size_t parts = w.n_splits > 1 ? rows * w.n_splits : 0;
-    w.before = kWorkspaceHeaderBytes;
-    w.list = w.before + (w.gather ? padded(sizeof(int) * (static_cast<size_t>(batch) + 1)) : 0);
-    w.part_o = w.list + padded(2 * sizeof(int4) * static_cast<size_t>(w.items));
+    w.part_o = kWorkspaceHeaderBytes;
     w.part_lse = w.part_o + padded(parts * head_dim * sizeof(float));
     w.bytes = w.part_lse + padded(parts * sizeof(float));
     return true;
@@ -288,7 +291,7 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
     if (head_dim > 128) return PHA_ERR_UNSUPPORTED;
     PagedPlan w;
     if (!paged_plan(w, batch, max_q, max_kv, total_q, n_heads, n_kv_heads, head_dim, dtype, window,
-                    sinks, paired) ||
+                    sinks, paired, page_size) ||
         (static_cast<int64_t>(n_pages) << shift) * n_kv_heads > INT32_MAX)
         return PHA_ERR_INVALID;
     if (dtype == PHA_BF16 && head_dim != 64 && head_dim != 128) return PHA_ERR_UNSUPPORTED;
@@ -327,19 +330,31 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
     p.part_o = reinterpret_cast<float*>(base + w.part_o);
     p.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     p.status = status;
+    if (!w.gather) {
+        cudaError_t e = launch_attn_rows(p, stream);
+        if (e == cudaSuccess && p.n_splits > 1) e = launch_attn_join(p, false, stream);
+        return of(e);
+    }
+    if (max_q == 0) return PHA_OK;
+    p.hdr = reinterpret_cast<WorkspaceHeader*>(base);
+    p.tiles = reinterpret_cast<int4*>(base + w.space.tiles);
+    p.starts = reinterpret_cast<int4*>(base + w.space.starts);
+    p.n_cta = kGatherCtas;
     p.pack = w.pack;
     p.tile_tokens = w.tile_tokens;
-    cudaError_t e;
-    if (w.gather) {
-        p.hdr = reinterpret_cast<WorkspaceHeader*>(base);
-        p.items = reinterpret_cast<int4*>(base + w.list);
-        e = launch_gather_plan(p, w.items, reinterpret_cast<int*>(base + w.before), false, stream);
-        if (e == cudaSuccess) e = launch_attn_gather(p, w.items, stream);
-    } else {
-        e = launch_attn_rows(p, stream);
-    }
-    if (e == cudaSuccess && p.n_splits > 1) e = launch_attn_join(p, dtype == PHA_BF16, stream);
-    return of(e);
+    p.box_rows = w.box_rows;
+    CUtensorMap tq, tk, tv;
+    const uint64_t rows = static_cast<uint64_t>(n_pages) << p.page_shift;
+    const uint64_t width = static_cast<uint64_t>(p.kv_heads) * head_dim;
+    const uint32_t box = w.box_rows < 8 ? 8 : w.box_rows;  // (below 8 the maps are not used)
+    if (!encode_pack_map(&tq, q, head_dim, p.heads, static_cast<uint64_t>(total_q) * p.mult,
+                         128 % p.pack == 0 ? p.pack : 1) ||
+        !encode_slot_map(&tk, k_pages, width, rows, box) || !encode_slot_map(&tv, v_pages, width, rows, box))
+        return PHA_ERR_CUDA;
+    if (launch_gather_plan(p, w.tiles, reinterpret_cast<int*>(base + w.space.before),
+                           reinterpret_cast<int64_t*>(base + w.space.steps), false, stream) != cudaSuccess)
+        return PHA_ERR_CUDA;
+    return of(launch_attn_gather(p, tq, tk, tv, stream));
 }
 
 }  // extern "C"

@@ -38,13 +38,23 @@ int real_window(int window, int max_len, int paired) {
 
 size_t padded(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// Work items of the forward (documents of any lengths up to max_len).
-int64_t fwd_items(int batch, int max_len, int n_heads, int n_kv_heads, int window, int sinks, int paired) {
-    const int mult = paired ? 2 : 1, heads = n_heads / mult;
-    const int pack = gather_pack(heads, n_kv_heads / mult);
+// Forward: row tiles, and tokens of one (documents of any lengths up to max_len).
+struct FwdPlan {
+    int pack, tile_tokens;
+    int64_t tiles;
+    GatherSpace space;
+};
+
+FwdPlan fwd_plan(int batch, int max_len, int n_heads, int n_kv_heads, int head_dim, int window, int sinks,
+                 int paired) {
+    const int mult = paired ? 2 : 1;
     const int64_t slots = static_cast<int64_t>(max_len) * mult;
-    window = real_window(window, max_len, paired);
-    return gather_items(batch, slots, slots * batch, gather_tile_tokens(pack, window, sinks), heads / pack, 1);
+    FwdPlan w;
+    w.pack = gather_pack(n_heads / mult, n_kv_heads / mult);
+    w.tile_tokens = gather_tile_tokens(w.pack, real_window(window, max_len, paired), sinks, 1);
+    w.tiles = gather_tiles(batch, slots, slots * batch, w.tile_tokens);
+    w.space = gather_space(batch, w.tiles, head_dim);
+    return w;
 }
 
 // Backward: header, per-document scratch and the largest work list (key tiles and far pieces), then
@@ -82,8 +92,7 @@ size_t pha_attn_sinks_workspace_bytes(int batch, int max_len, int n_heads, int n
                                       int head_dim, int window, int sinks, int paired) {
     if (shape_status(batch, max_len, 0, n_heads, n_kv_heads, head_dim, PHA_F32, sinks, paired, 0.f) != PHA_OK)
         return 0;
-    return kWorkspaceHeaderBytes + padded(sizeof(int) * (static_cast<size_t>(batch) + 1)) +
-           2 * sizeof(int4) * static_cast<size_t>(fwd_items(batch, max_len, n_heads, n_kv_heads, window, sinks, paired));
+    return fwd_plan(batch, max_len, n_heads, n_kv_heads, head_dim, window, sinks, paired).space.bytes;
 }
 
 size_t pha_attn_sinks_bwd_workspace_bytes(int batch, int max_len, int total_tokens, int n_heads,
@@ -129,20 +138,30 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
     p.window = real_window(window, max_len, paired);
     p.sinks = sinks;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
-    p.n_splits = 1;
-    p.pack = gather_pack(p.heads, p.kv_heads);
-    p.tile_tokens = gather_tile_tokens(p.pack, p.window, p.sinks);
+    const FwdPlan w = fwd_plan(batch, max_len, n_heads, n_kv_heads, head_dim, window, sinks, paired);
     auto* base = static_cast<uint8_t*>(workspace);
     p.hdr = reinterpret_cast<WorkspaceHeader*>(base);
-    auto* before = reinterpret_cast<int*>(base + kWorkspaceHeaderBytes);
+    p.tiles = reinterpret_cast<int4*>(base + w.space.tiles);
+    p.starts = reinterpret_cast<int4*>(base + w.space.starts);
+    p.part_o = reinterpret_cast<float*>(base + w.space.part_o);
+    p.part_lse = reinterpret_cast<float*>(base + w.space.part_lse);
+    p.n_cta = kGatherCtas;
+    p.pack = w.pack;
+    p.tile_tokens = w.tile_tokens;
+    p.box_rows = kBlockN;
     const bool tc = dtype == PHA_BF16;
-    if (tc)
-        p.items = reinterpret_cast<int4*>(base + kWorkspaceHeaderBytes +
-                                          padded(sizeof(int) * (static_cast<size_t>(batch) + 1)));
-    const int64_t items = fwd_items(batch, max_len, n_heads, n_kv_heads, window, sinks, paired);
-    cudaError_t e = launch_gather_plan(p, items < INT32_MAX ? items : INT32_MAX, before, true, stream);
-    if (e == cudaSuccess && have) e = tc ? launch_attn_gather(p, items, stream) : launch_attn_rows(p, stream);
-    return of(e);
+    if (launch_gather_plan(p, tc ? w.tiles : 0, reinterpret_cast<int*>(base + w.space.before),
+                           reinterpret_cast<int64_t*>(base + w.space.steps), true, stream) != cudaSuccess)
+        return PHA_ERR_CUDA;
+    if (!have || max_len == 0) return PHA_OK;
+    if (!tc) return of(launch_attn_rows(p, stream));
+    CUtensorMap tq, tk, tv;
+    const uint64_t rows = static_cast<uint64_t>(total_tokens) * p.mult;
+    const uint64_t width = static_cast<uint64_t>(p.kv_heads) * head_dim;
+    if (!encode_pack_map(&tq, q, head_dim, p.heads, rows, 128 % p.pack == 0 ? p.pack : 1) ||
+        !encode_slot_map(&tk, k, width, rows) || !encode_slot_map(&tv, v, width, rows))
+        return PHA_ERR_CUDA;
+    return of(launch_attn_gather(p, tq, tk, tv, stream));
 }
 
 pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const void* o,

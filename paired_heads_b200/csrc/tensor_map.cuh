@@ -55,4 +55,20 @@ inline bool encode_u8_map(CUtensorMap* map, const void* base, uint64_t width, ui
     return r == CUDA_SUCCESS;
 }
 
+// 3-D bf16 map over q [rows][heads][hd] whose box is 64 columns of `pack` heads of 128 / pack rows (pack
+// divides 128): a query tile with its rows in (row, head) order. 128-byte swizzle, zero fill outside.
+inline bool encode_pack_map(CUtensorMap* map, const void* base, uint64_t hd, uint64_t heads, uint64_t rows,
+                            uint32_t pack) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
+    if (!encode) return false;
+    cuuint64_t dims[3] = {hd, heads, rows};
+    cuuint64_t strides[2] = {hd * 2, heads * hd * 2};
+    cuuint32_t box[3] = {64, pack, 128 / pack};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace pha
