@@ -182,7 +182,14 @@ struct GBars {
 constexpr int kGBarBytes = 1280;
 static_assert(sizeof(GBars) <= kGBarBytes, "barrier block");
 
-template <int HD, bool PAGED>
+// Windows up to this run the NARROW form (4 x 8192 tokens, 4 sinks, us, it and the other: 32 / 8 heads of
+// 128, window 64: 148 / 150, 256: 214 / 239, 384: 314 / 320, 1024: 372 / 372; 12 heads of 64, window 128:
+// 150 / 150, 256: 193 / 186, 512: 238 / 219, 1024: 287 / 256).
+constexpr int kNarrowWindow = 256;
+
+// NARROW: windows so short that most tiles are masked; masked tiles then go chunk by
+// chunk and skip the hidden chunks. With long windows the loop's latencies cost more than it skips.
+template <int HD, bool PAGED, bool NARROW>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_gather_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const GatherProblem p, const int p_inv) {
@@ -268,19 +275,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto place = [&](uint32_t tile, int row) -> uint32_t {
             return tile + unit_off + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
         };
-        // the 128 rows of one tile whose pool rows are idx[kk] of lane row % 32 (negative: zeros)
-        auto load_keys = [&](const __nv_bfloat16* src, uint32_t tile, const int (&idx)[4], int head) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                // 32 / kRpi row groups per 32 rows, dealt out to the warps in turn across the tile
-                const int from = (w + kLoadWarps * 32 - kk * (32 / kRpi)) % kLoadWarps;
-#pragma unroll 6
-                for (int j = from; j < 32 / kRpi; j += kLoadWarps) {
-                    const int r32 = j * kRpi + row_in;
-                    const int x = __shfl_sync(0xffffffffu, idx[kk], r32);
-                    const int64_t at = (static_cast<int64_t>(x < 0 ? 0 : x) * p.kv_heads + head) * HD;
-                    cp_async_16_zfill(place(tile, 32 * kk + r32), src + at, x < 0 ? 0u : 16u);
-                }
+        // The 128 rows of a K and a V tile whose pool rows are i0 .. i3 of lane row % 32 for the four blocks
+        // of 32 rows (negative: zeros). A small loop: unrolled, this code ran cold every time and took 5,000
+        // cycles a tile.
+        auto load_keys = [&](uint32_t k_tile, uint32_t v_tile, int i0, int i1, int i2, int i3, int head) {
+#pragma unroll 2
+            for (int j = w; j < kBlockN / kRpi; j += kLoadWarps) {
+                const int row = j * kRpi + row_in;
+                const int block = row >> 5;
+                const int mine = block == 0 ? i0 : (block == 1 ? i1 : (block == 2 ? i2 : i3));
+                const int x = __shfl_sync(0xffffffffu, mine, row & 31);
+                const int64_t at = (static_cast<int64_t>(x < 0 ? 0 : x) * p.kv_heads + head) * HD;
+                cp_async_16_zfill(place(k_tile, row), k_all + at, x < 0 ? 0u : 16u);
+                cp_async_16_zfill(place(v_tile, row), v_all + at, x < 0 ? 0u : 16u);
             }
         };
         // 128 consecutive columns by TMA, a lane per box; a page that is none reads as zeros (a row behind
@@ -404,13 +411,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             idx[kk] = static_cast<int>(row);
                         }
                     }
-                    ok = acquire(&bars->k_empty[sk], ((kc / L::kKStages) & 1) ^ 1);
+                    ok = acquire(&bars->k_empty[sk], ((kc / L::kKStages) & 1) ^ 1) &&
+                         acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
                     if (!ok) break;
-                    load_keys(k_all, sbase + L::kOffK + sk * L::kKV, idx, head);
+                    load_keys(sbase + L::kOffK + sk * L::kKV, sbase + L::kOffV + sv * L::kKV, idx[0], idx[1], idx[2],
+                              idx[3], head);
                     cp_async_arrive(&bars->k_full[sk]);
-                    ok = acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
-                    if (!ok) break;
-                    load_keys(v_all, sbase + L::kOffV + sv * L::kKV, idx, head);
                     cp_async_arrive(&bars->v_full[sv]);
                 }
                 // the second sub-tile's Q after the first key tile: its slot is free only when the previous
@@ -605,57 +611,108 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 ++s_cnt;
                 tc_fence_after();
-                uint32_t v[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, v + 32 * c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) regs_after_wait(v + 32 * c);
-                if (kSepP) {
-                    tc_fence_before();  // S_r may be overwritten from here on
-                    mbar_arrive(&bars->s_free[r]);
-                }
-                if (t < t_full || t >= t_end) {
-                    uint32_t vis[4];  // bit e of vis[c]: column 32 c + e of the tile is visible to this row
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int cb = t * kBlockN + 32 * c;
-                        const uint32_t below = p.window > 0 ? low_bits(c_hi + 1 - p.window - cb) : 0u;
-                        const uint32_t seen = low_bits(c_hi + 1 - cb) & (~below | low_bits(ns - cb));
-                        vis[c] = seen | (low_bits(total - cb) & ~low_bits(n_w - cb));
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[32 * c + e] = ((vis[c] >> e) & 1u) ? v[32 * c + e] : __float_as_uint(-INFINITY);
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) mx = fmaxf(mx, chunk_max<kMaskNone>(v + 32 * c, 0, 0, 0));
-                const float m_new = fmaxf(m, mx * scale_log2);
-                // the reference stays until the maximum has grown by more than 2^8: O / l and the lse
-                // are exact for any reference
-                const bool rescale = m_new > m + 8.0f;
-                const float alpha = rescale ? ex2(m - m_new) : 1.0f;
-                if (rescale) m = m_new;
-                const float neg_m = (m == -INFINITY) ? 0.f : -m;
-                const uint64_t negm2 = f32x2(neg_m, neg_m);
                 uint64_t sum_a = f32x2(0.f, 0.f), sum_b = f32x2(0.f, 0.f);
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    chunk_exp<kMaskNone>(v + 32 * c, 0, 0, 0, scale2, negm2, sum_a, sum_b, pk + 16 * (c & 1));
-                    if (c == 1 && kSepP && pv_seen < s_cnt - 1) {
-                        // hd 64: the last P V reads P_r and adds into O_r; it must be complete before P_r is
-                        // overwritten and O_r rescaled
+                float mx = -INFINITY, alpha = 1.0f;
+                uint64_t negm2 = 0;
+                bool rescale = false;
+                // After the scores' maximum is known: the reference stays until the maximum has grown by more
+                // than 2^8 (O / l and the lse are exact for any reference).
+                auto new_reference = [&]() {
+                    const float m_new = fmaxf(m, mx * scale_log2);
+                    rescale = m_new > m + 8.0f;
+                    alpha = rescale ? ex2(m - m_new) : 1.0f;
+                    if (rescale) m = m_new;
+                    const float neg_m = (m == -INFINITY) ? 0.f : -m;
+                    negm2 = f32x2(neg_m, neg_m);
+                };
+                // hd 64: the last P V reads P_r and adds into O_r; it must be complete before P_r is overwritten
+                // and O_r rescaled
+                auto wait_pv = [&]() {
+                    if (kSepP && pv_seen < s_cnt - 1) {
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[r], pv_seen & 1, abort_flag, dev_status));
                         ++pv_seen;
                         tc_fence_after();
                     }
-                    if (c & 1) {
-                        tmem_st16(tm_p + 16 * (c - 1), pk);
-                        tmem_st16(tm_p + 16 * c, pk + 16);
+                };
+                const bool masked = t < t_full || t >= t_end;
+                auto visible = [&](int c) -> uint32_t {  // bit e: column 32 c + e of the tile is visible
+                    const int cb = t * kBlockN + 32 * c;
+                    const uint32_t below = p.window > 0 ? low_bits(c_hi + 1 - p.window - cb) : 0u;
+                    const uint32_t seen = low_bits(c_hi + 1 - cb) & (~below | low_bits(ns - cb));
+                    return seen | (low_bits(total - cb) & ~low_bits(n_w - cb));
+                };
+                if (!NARROW || !masked) {
+                    // the 128 scores at once, in registers
+                    uint32_t v[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, v + 32 * c);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) regs_after_wait(v + 32 * c);
+                    if (kSepP) {
+                        tc_fence_before();  // S_r may be overwritten from here on
+                        mbar_arrive(&bars->s_free[r]);
+                    }
+                    if (!NARROW && masked) {
+                        uint32_t vis[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) vis[c] = visible(c);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                v[32 * c + e] = ((vis[c] >> e) & 1u) ? v[32 * c + e] : __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx = fmaxf(mx, chunk_max<kMaskNone>(v + 32 * c, 0, 0, 0));
+                    new_reference();
+                    // P = 2^(s scale log2 e - m), written after the whole row was read (it may share S's columns)
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        chunk_exp<kMaskNone>(v + 32 * c, 0, 0, 0, scale2, negm2, sum_a, sum_b, pk + 16 * (c & 1));
+                        if (c == 1) wait_pv();
+                        if (c & 1) {
+                            tmem_st16(tm_p + 16 * (c - 1), pk);
+                            tmem_st16(tm_p + 16 * c, pk + 16);
+                        }
+                    }
+                } else {
+                    // its 32-column chunks in loops, twice (maximum, then weights), those that no row of the warp
+                    // sees skipped
+                    auto scores = [&](int c, uint32_t vis, uint32_t (&v)[32]) {
+                        tmem_ld32(tm_s + 32 * c, v);
+                        tmem_wait_ld();
+                        regs_after_wait(v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = ((vis >> e) & 1u) ? v[e] : __float_as_uint(-INFINITY);
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t vis = visible(c);
+                        if (!__any_sync(0xffffffffu, vis != 0u)) continue;
+                        uint32_t v[32];
+                        scores(c, vis, v);
+                        mx = fmaxf(mx, chunk_max<kMaskNone>(v, 0, 0, 0));
+                    }
+                    new_reference();
+                    wait_pv();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {  // (P's columns lie at or before those of scores already read)
+                        const uint32_t vis = visible(c);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                        if (__any_sync(0xffffffffu, vis != 0u)) {
+                            uint32_t v[32];
+                            scores(c, vis, v);
+                            chunk_exp<kMaskNone>(v, 0, 0, 0, scale2, negm2, sum_a, sum_b, pk);
+                        }
+                        tmem_st16(tm_p + 16 * c, pk);
+                    }
+                    if (kSepP) {
+                        tc_fence_before();
+                        mbar_arrive(&bars->s_free[r]);
                     }
                 }
                 if (!ok) break;
@@ -805,11 +862,11 @@ __global__ void __launch_bounds__(256) attn_join_cuts_kernel(GatherProblem p, in
     }
 }
 
-template <int HD, bool PAGED>
+template <int HD, bool PAGED, bool NARROW>
 cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t stream) {
     constexpr int kSmem = TcLayout<HD>::kOffBar + kGBarBytes + 1024;  // + slack to align to 1024
-    cudaError_t e = cudaFuncSetAttribute(attn_gather_kernel<HD, PAGED>,
+    cudaError_t e = cudaFuncSetAttribute(attn_gather_kernel<HD, PAGED, NARROW>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int p_inv = (65536 + p.pack - 1) / p.pack;
@@ -823,7 +880,7 @@ cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_gather_kernel<HD, PAGED>, tq, tk, tv, p, p_inv);
+    e = cudaLaunchKernelEx(&cfg, attn_gather_kernel<HD, PAGED, NARROW>, tq, tk, tv, p, p_inv);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.n_cta, (p.tile_tokens * p.pack + 31) / 32);
     cfg.blockDim = dim3(256);
@@ -835,13 +892,15 @@ cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, cons
 
 cudaError_t launch_attn_gather(const GatherProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const CUtensorMap& tm_v, cudaStream_t stream) {
-    if (p.head_dim == 128)
-        return p.kv_lens ? launch_gather_hd<128, true>(p, tm_q, tm_k, tm_v, stream)
-                         : launch_gather_hd<128, false>(p, tm_q, tm_k, tm_v, stream);
-    if (p.head_dim == 64)
-        return p.kv_lens ? launch_gather_hd<64, true>(p, tm_q, tm_k, tm_v, stream)
-                         : launch_gather_hd<64, false>(p, tm_q, tm_k, tm_v, stream);
-    return cudaErrorInvalidValue;
+    if (p.head_dim != 64 && p.head_dim != 128) return cudaErrorInvalidValue;
+    const bool paged = p.kv_lens != nullptr, narrow = p.window > 0 && p.window <= kNarrowWindow;
+    auto* const launch =
+        p.head_dim == 128
+            ? (paged ? (narrow ? launch_gather_hd<128, true, true> : launch_gather_hd<128, true, false>)
+                     : (narrow ? launch_gather_hd<128, false, true> : launch_gather_hd<128, false, false>))
+            : (paged ? (narrow ? launch_gather_hd<64, true, true> : launch_gather_hd<64, true, false>)
+                     : (narrow ? launch_gather_hd<64, false, true> : launch_gather_hd<64, false, false>));
+    return launch(p, tm_q, tm_k, tm_v, stream);
 }
 
 }  // namespace pha
