@@ -195,6 +195,11 @@ cudaError_t launch_gather_plan(const GatherProblem& p, int64_t max_tiles, int* b
 cudaError_t launch_attn_gather(const GatherProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const CUtensorMap& tm_v, cudaStream_t stream);
 
+// bf16, head_dim 64 / 128, few rows: at most kDecodeRows (new slots times a group's heads) a sequence;
+// block per (split, kv head, sequence).
+constexpr int kDecodeRows = 16;
+cudaError_t launch_attn_decode(const GatherProblem& p, cudaStream_t stream);
+
 // float32 on CUDA cores: one warp per (row, split).
 cudaError_t launch_attn_rows(const GatherProblem& p, cudaStream_t stream);
 

@@ -199,9 +199,12 @@ pha_status pha_cache_compact(int32_t* page_table, int max_pages, int n_seqs, int
 namespace {
 
 constexpr int kRowsSplitKeys = 1024;  // key columns of one warp's split (float32)
+constexpr int kDecodeBlocks = 8 * kGatherCtas;  // blocks of the decoding kernel to aim at
+constexpr int kDecodeMinSplit = 256, kDecodeMaxSplit = 1024;
 
 struct PagedPlan {
     bool gather;                 // the tensor-core kernel with a plan
+    bool decode;                 // few rows per sequence
     int window, sinks;           // as the kernels take them
     int n_splits, split_keys;
     int pack, tile_tokens, box_rows;
@@ -232,7 +235,9 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
         const int64_t seen = static_cast<int64_t>(window) + static_cast<int64_t>(max_q) * mult + sinks;
         most = seen < most ? seen : most;
     }
-    w.gather = dtype == PHA_BF16;
+    const int64_t rows_each = static_cast<int64_t>(max_q) * mult * (heads / kv_heads);
+    w.decode = dtype == PHA_BF16 && rows_each <= kDecodeRows && batch <= 65535 && kv_heads <= 65535;
+    w.gather = dtype == PHA_BF16 && !w.decode;
     if (w.gather) {
         // A TMA box stays in one page. Without a window columns begin at position 0 and it may be a whole
         // tile; with one they begin at a multiple of the box, so it is kept to 32 rows (16 of the
@@ -252,6 +257,12 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
         return true;
     }
     w.split_keys = kRowsSplitKeys;
+    if (w.decode) {
+        // key ranges short enough that the blocks fill the GPU a few times over (ragged histories even
+        // out), but not so short that joining them costs more than it spreads
+        const int64_t want = most * batch * kv_heads / kDecodeBlocks;
+        w.split_keys = static_cast<int>(want < kDecodeMinSplit ? kDecodeMinSplit : (want > kDecodeMaxSplit ? kDecodeMaxSplit : (want + 63) / 64 * 64));
+    }
     w.n_splits = static_cast<int>((most + w.split_keys - 1) / w.split_keys);
     if (w.n_splits < 1) w.n_splits = 1;
     const size_t rows = static_cast<size_t>(total_q) * n_heads;
@@ -331,8 +342,8 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
     p.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     p.status = status;
     if (!w.gather) {
-        cudaError_t e = launch_attn_rows(p, stream);
-        if (e == cudaSuccess && p.n_splits > 1) e = launch_attn_join(p, false, stream);
+        cudaError_t e = w.decode ? launch_attn_decode(p, stream) : launch_attn_rows(p, stream);
+        if (e == cudaSuccess && p.n_splits > 1) e = launch_attn_join(p, w.decode, stream);
         return of(e);
     }
     if (max_q == 0) return PHA_OK;
