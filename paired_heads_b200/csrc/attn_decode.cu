@@ -84,15 +84,24 @@ __global__ void __launch_bounds__(32 * kWarps) attn_decode_kernel(const GatherPr
     const __nv_bfloat16* k_all = static_cast<const __nv_bfloat16*>(p.k) + static_cast<int64_t>(g) * HD + unit * 8;
     const __nv_bfloat16* v_all = static_cast<const __nv_bfloat16*>(p.v) + static_cast<int64_t>(g) * HD + unit * 8;
     const int64_t stride = static_cast<int64_t>(p.kv_heads) * HD;
-    // copies of step `step` into stage `st` (one group, empty past the last step)
+    // The table entry of this lane's key of a step, read one step ahead of the copies that need it.
+    auto entry_of = [&](int step) -> int {
+        const int col = c0 + step * kStepKeys + (lane & 15);
+        if (col >= c1) return -1;
+        return __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + (col_pos(cols, col) >> p.page_shift));
+    };
+    int entry = entry_of(warp);
+    // copies of step `step` (the next one that `entry` is for) into stage `st`: one group, empty past the
+    // last step
     auto fetch = [&](int step, int st) {
         if (step < steps) {
             const int col = c0 + step * kStepKeys + (lane & 15);
-            int mine = -1;
-            if (col < c1) {
-                mine = static_cast<int>(key_row<true>(p, b, 0, col_pos(cols, col)));
-                if (mine < 0 && p.status) atomicMax(p.status, DEV_BAD_PAGE);
-            }
+            const int page = entry;
+            entry = entry_of(step + kWarps);
+            const bool is_page = page >= 0 && page < p.n_pages;
+            if (col < c1 && !is_page && p.status) atomicMax(p.status, DEV_BAD_PAGE);
+            const int in = col_pos(cols, col) & ((1 << p.page_shift) - 1);
+            const int mine = col < c1 && is_page ? (page << p.page_shift) + in : -1;
             const uint32_t k_st = ring + st * stage_bytes<HD>(), v_st = k_st + kStepKeys * kRowBytes;
 #pragma unroll
             for (int i = 0; i < kStepKeys / kRpi; ++i) {

@@ -199,8 +199,7 @@ pha_status pha_cache_compact(int32_t* page_table, int max_pages, int n_seqs, int
 namespace {
 
 constexpr int kRowsSplitKeys = 1024;  // key columns of one warp's split (float32)
-constexpr int kDecodeBlocks = 8 * kGatherCtas;  // blocks of the decoding kernel to aim at
-constexpr int kDecodeMinSplit = 256, kDecodeMaxSplit = 1024;
+constexpr int kDecodeMinSplit = 512, kDecodeMaxSplit = 2048;  // keys of a block of the decoding kernel
 
 struct PagedPlan {
     bool gather;                 // the tensor-core kernel with a plan
@@ -258,10 +257,15 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
     }
     w.split_keys = kRowsSplitKeys;
     if (w.decode) {
-        // key ranges short enough that the blocks fill the GPU a few times over (ragged histories even
-        // out), but not so short that joining them costs more than it spreads
-        const int64_t want = most * batch * kv_heads / kDecodeBlocks;
-        w.split_keys = static_cast<int>(want < kDecodeMinSplit ? kDecodeMinSplit : (want > kDecodeMaxSplit ? kDecodeMaxSplit : (want + 63) / 64 * 64));
+        // One wave of blocks where the (sequence, kv head) pairs leave room for several ranges each; ranges
+        // of at most kDecodeMaxSplit keys where they do not, so that long histories do not outlast the
+        // short ones' blocks; never shorter than kDecodeMinSplit (a block's start and the join cost
+        // as much as a few hundred keys).
+        const int64_t units = static_cast<int64_t>(batch) * kv_heads;
+        const int64_t fit = kGatherCtas * (head_dim == 128 ? 2 : 4) / units;
+        int64_t keys = fit > 1 ? (most + fit - 1) / fit : most;
+        keys = (keys + 63) / 64 * 64;
+        w.split_keys = static_cast<int>(keys < kDecodeMinSplit ? kDecodeMinSplit : (keys > kDecodeMaxSplit ? kDecodeMaxSplit : keys));
     }
     w.n_splits = static_cast<int>((most + w.split_keys - 1) / w.split_keys);
     if (w.n_splits < 1) w.n_splits = 1;

@@ -395,11 +395,23 @@ def pha_attn_status(workspace, stream=None):
 # that the elements are contiguous. A tensor on another device than the current one is fine: the
 # call is made on the tensor's device.
 
+_torch = None
+
+
+def _lazy_torch():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
 def _want(name, t, dtype, *shape):
-    """t is a contiguous tensor of this dtype and shape (None: any extent)."""
-    if t.dtype != dtype:
+    """t is a contiguous tensor of this dtype and shape."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
@@ -407,33 +419,34 @@ def _want(name, t, dtype, *shape):
 
 def _run(fn, args, stream, first, *others):
     """Calls the library on the device of `first`, which the other tensors must share."""
-    import torch
-
-    dev = first.device
-    if dev.type != "cuda":
+    cuda = _lazy_torch().cuda
+    index = first.get_device()
+    if index < 0:
         raise ValueError(f"{fn}: tensors not on a CUDA device")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
     call = getattr(_lib, fn)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn, call(*args, _stream(stream, first)))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn, call(*args, _stream(stream, first)))
+    if cuda.current_device() != index:
+        with cuda.device(index):
+            return _check(fn, call(*args, _stream(stream, first)))
+    if stream is None:
+        stream = cuda.current_stream().cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    rc = call(*args, stream)
+    if rc != 0:
+        _check(fn, rc)
 
 
 def _int32():
-    import torch
-
-    return torch.int32
+    return _lazy_torch().int32
 
 
-def _attn_shape(q, k, v, o, lse):
-    """Checks q, k, v, o, lse of a packed call; (tokens, heads, kv heads, head_dim, dtype code)."""
-    import torch
-
-    dt = _dtype_code(q)
+def _attn_shape(q, k, o, lse):
+    """Checks q, o, lse of a call; (tokens, heads, kv heads, head_dim, dtype code)."""
+    torch = _lazy_torch()
+    dt = PHA_BF16 if q.dtype is torch.bfloat16 else _dtype_code(q)
     t, h, hd = q.shape
     hkv = k.shape[-2]
     _want("q", q, q.dtype, t, h, hd)
@@ -466,10 +479,10 @@ def pha_attn_sinks_fwd(q, k, v, cu_seqlens, max_len: int, o, lse, workspace, *, 
                        sinks: int, paired: bool = False, scale: float = 0.0, stream=None):
     """Causal varlen attention with a sliding window and `sinks` visible first slots per document,
     into o (like q) and lse [T][H] float32 (or None). pha_attn_status(workspace) reports."""
-    t, h, hkv, hd, dt = _attn_shape(q, k, v, o, lse)
+    t, h, hkv, hd, dt = _attn_shape(q, k, o, lse)
     _want("k", k, q.dtype, t, hkv, hd)
     _want("v", v, q.dtype, t, hkv, hd)
-    _want("cu_seqlens", cu_seqlens, _int32(), None)
+    _want("cu_seqlens", cu_seqlens, _int32(), cu_seqlens.shape[0])
     _run("pha_attn_sinks_fwd",
          (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
           max_len, t, h, hkv, hd, dt, window, sinks, int(paired), scale, o.data_ptr(), _ptr(lse),
@@ -480,11 +493,11 @@ def pha_attn_sinks_bwd(q, k, v, o, lse, dout, cu_seqlens, max_len: int, dq, dk, 
                        window: int, sinks: int, paired: bool = False, scale: float = 0.0,
                        stream=None):
     """Backward of pha_attn_sinks_fwd (o, lse: its outputs): dq, dk, dv for dout."""
-    t, h, hkv, hd, dt = _attn_shape(q, k, v, o, lse)
+    t, h, hkv, hd, dt = _attn_shape(q, k, o, lse)
     for name, x, heads in (("k", k, hkv), ("v", v, hkv), ("dout", dout, h), ("dq", dq, h),
                            ("dk", dk, hkv), ("dv", dv, hkv)):
         _want(name, x, q.dtype, t, heads, hd)
-    _want("cu_seqlens", cu_seqlens, _int32(), None)
+    _want("cu_seqlens", cu_seqlens, _int32(), cu_seqlens.shape[0])
     _run("pha_attn_sinks_bwd",
          (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), dout.data_ptr(),
           cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, max_len, t, h, hkv, hd, dt, window, sinks,
@@ -510,20 +523,21 @@ def pha_attn_paged_fwd(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, max
     """Attention of each sequence's new tokens q over its paged cache (k_pages, v_pages
     [pages][page_size][Hkv][hd], page_table [batch][max_pages], kv_lens [batch] with the new tokens
     included) into o and lse (or None). status: int32[1], raised on bad lengths or pages."""
-    t, h, hkv, hd, dt = _attn_shape(q, k_pages, v_pages, o, lse)
+    t, h, hkv, hd, dt = _attn_shape(q, k_pages, o, lse)
     n_pages, page = k_pages.shape[:2]
     batch = cu_seqlens.shape[0] - 1
     _want("k_pages", k_pages, q.dtype, n_pages, page, hkv, hd)
     _want("v_pages", v_pages, q.dtype, n_pages, page, hkv, hd)
     i32 = _int32()
-    _want("page_table", page_table, i32, batch, None)
+    max_pages = page_table.shape[-1]
+    _want("page_table", page_table, i32, batch, max_pages)
     _want("cu_seqlens", cu_seqlens, i32, batch + 1)
     _want("kv_lens", kv_lens, i32, batch)
     if status is not None:
         _want("status", status, i32, 1)
     _run("pha_attn_paged_fwd",
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-          page_table.shape[1], n_pages, page, cu_seqlens.data_ptr(), kv_lens.data_ptr(), batch,
+          max_pages, n_pages, page, cu_seqlens.data_ptr(), kv_lens.data_ptr(), batch,
           max_q, max_kv, t, h, hkv, hd, dt, window, sinks, int(paired), scale, o.data_ptr(),
           _ptr(lse), workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream, q, k_pages,
          v_pages, page_table, cu_seqlens, kv_lens, o, lse, workspace, status)
@@ -540,14 +554,15 @@ def pha_cache_append(k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, *,
     _want("k_pages", k_pages, k.dtype, n_pages, page, hkv, hd)
     _want("v_pages", v_pages, k.dtype, n_pages, page, hkv, hd)
     i32 = _int32()
-    _want("page_table", page_table, i32, batch, None)
+    max_pages = page_table.shape[-1]
+    _want("page_table", page_table, i32, batch, max_pages)
     _want("cu_seqlens", cu_seqlens, i32, batch + 1)
     _want("kv_lens", kv_lens, i32, batch)
     if status is not None:
         _want("status", status, i32, 1)
     _run("pha_cache_append",
          (k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-          page_table.data_ptr(), page_table.shape[1], n_pages, page, cu_seqlens.data_ptr(),
+          page_table.data_ptr(), max_pages, n_pages, page, cu_seqlens.data_ptr(),
           kv_lens.data_ptr(), batch, t, hkv, hd, k.element_size(), _ptr(status)), stream, k, v,
          k_pages, v_pages, page_table, cu_seqlens, kv_lens, status)
 
@@ -563,7 +578,7 @@ def _cache_state(page_table, kv_lens, page_refs, status):
     _want("page_table", page_table, i32, n_seqs, max_pages)
     if kv_lens is not None:
         _want("kv_lens", kv_lens, i32, n_seqs)
-    _want("page_refs", page_refs, i32, None)
+    _want("page_refs", page_refs, i32, page_refs.shape[0])
     if status is not None:
         _want("status", status, i32, 1)
     return max_pages, n_seqs, page_refs.shape[0]
