@@ -40,6 +40,11 @@ constexpr int kLanesPerRow = 8;
 constexpr int kRowsPerBlock = kBwdThreads / kLanesPerRow;  // 32
 constexpr int kStage = 32;                                // rows staged per chunk
 
+// Pairs of a row's loop in flight at a time: their dot products' shuffles are a chain of about 250
+// cycles each. As many as the registers allow.
+template <int HP>
+constexpr int kUnroll = HP == 32 ? 4 : (HP == 64 ? 2 : 1);
+
 template <typename T>
 __device__ __forceinline__ float ld(const T* p);
 template <>
@@ -208,7 +213,11 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
             stage_rows<HP>(vs, vg, c0, n, kstride, hd);
             __syncthreads();
             if ((c0 + n <= wj0 && p.sinks == 0) || c0 >= wj1) continue;  // warp-uniform
-            for (int jj = 0; jj < n; ++jj) {
+            // only what the warp's rows see of the chunk
+            const int from = p.sinks == 0 && wj0 > c0 ? static_cast<int>(wj0 - c0) : 0;
+            const int to = wj1 < c0 + n ? static_cast<int>(wj1 - c0) : n;
+#pragma unroll kUnroll<HP>
+            for (int jj = from; jj < to; ++jj) {
                 const long long j = c0 + jj;
                 const float4* kr = reinterpret_cast<const float4*>(ks + jj * HP);
                 const float4* vr = reinterpret_cast<const float4*>(vs + jj * HP);
@@ -260,8 +269,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
         i1 = hi;
         if (p.causal) {
             i0 = j;
-            // (a sink is seen by every later query of its document)
-            if (p.window > 0 && j - lo >= p.sinks && j + p.window < i1) i1 = j + p.window;
+            if (p.window > 0 && j + p.window < i1) i1 = j + p.window;
         }
     }
     if (threadIdx.x == 0) {
@@ -299,7 +307,11 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
             }
             __syncthreads();
             if (c0 + n <= wi0 || c0 >= wi1) continue;  // warp-uniform
-            for (int ii = 0; ii < n; ++ii) {
+            // only what the warp's rows see of the chunk
+            const int from = wi0 > c0 ? static_cast<int>(wi0 - c0) : 0;
+            const int to = wi1 < c0 + n ? static_cast<int>(wi1 - c0) : n;
+#pragma unroll kUnroll<HP>
+            for (int ii = from; ii < to; ++ii) {
                 const long long i = c0 + ii;
                 const float4* qr = reinterpret_cast<const float4*>(qs + ii * HP);
                 const float4* gr = reinterpret_cast<const float4*>(gs + ii * HP);
@@ -327,6 +339,90 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
         store_row<NC>(dk + krow * hd, ak, hd, r8);
         store_row<NC>(dv + krow * hd, av, hd, r8);
     }
+}
+
+// Sinks (float32): what the queries behind key j's window add to dk_j, dv_j, for the first p.sinks slots
+// of every document. Block (document, kv head, sink): eight lanes a query of some head of the
+// group; the sums are joined in order and added to the window's part. (Letting the
+// kernel above walk whole documents for these rows left a few blocks with a long serial loop: 58 us
+// against 17 for 232 tokens of 4 heads, window 9, 3 sinks.)
+template <int HP>
+__global__ void __launch_bounds__(kBwdThreads) attn_bwd_far_kernel(AttnProblem p, const float* __restrict__ dout,
+                                                                   const float* __restrict__ dsum,
+                                                                   float* __restrict__ dk, float* __restrict__ dv) {
+    constexpr int NC = HP / (4 * kLanesPerRow), kWarps = kBwdThreads / 32;
+    if (p.checked && p.checked->status != DEV_OK) return;
+    __shared__ float part[kWarps][2][HP];
+    const int warp = threadIdx.x >> 5, r8 = threadIdx.x % kLanesPerRow;
+    const int g = blockIdx.y, hd = p.head_dim, H = p.heads, G = H / p.kv_heads;
+    const int64_t lo = static_cast<int64_t>(p.cu_seqlens[blockIdx.x]) * p.slot_mult;
+    const int64_t hi = static_cast<int64_t>(p.cu_seqlens[blockIdx.x + 1]) * p.slot_mult;
+    const int64_t j = lo + blockIdx.z, i0 = j + p.window;  // the first query behind j's window
+    if (j >= hi || i0 >= hi) return;
+    const float scale2 = p.scale * 1.4426950408889634f;
+    const int64_t krow = (j * p.kv_heads + g) * hd;
+    float4 kj[NC], vj[NC], ak[NC], av[NC];
+    load_row<NC>(kj, static_cast<const float*>(p.k) + krow, hd, r8, true);
+    load_row<NC>(vj, static_cast<const float*>(p.v) + krow, hd, r8, true);
+#pragma unroll
+    for (int t = 0; t < NC; ++t) ak[t] = av[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t n = (hi - i0) * G;
+    for (int64_t base = 0; base < n; base += kRowsPerBlock) {  // (whole warps: the sums shuffle)
+        const int64_t x = base + threadIdx.x / kLanesPerRow;
+        const bool in = x < n;
+        const int64_t row = in ? (i0 + x / G) * H + g * G + x % G : 0;
+        float4 q[NC], go[NC];
+        load_row<NC>(q, static_cast<const float*>(p.q) + row * hd, hd, r8, in);
+        load_row<NC>(go, dout + row * hd, hd, r8, in);
+        const float lse = in ? p.lse[row] : 0.f, d = in ? dsum[row] : 0.f;
+        float s = 0.f, dp = 0.f;
+#pragma unroll
+        for (int t = 0; t < NC; ++t) {
+            s = dot4(kj[t], q[t], s);
+            dp = dot4(vj[t], go[t], dp);
+        }
+        group_sum2(s, dp);
+        const float w = in ? exp2f(fmaf(s, scale2, -lse * 1.4426950408889634f)) : 0.f;
+        const float ds = w * (dp - d) * p.scale;
+#pragma unroll
+        for (int t = 0; t < NC; ++t) {
+            axpy4(ak[t], ds, q[t]);
+            axpy4(av[t], w, go[t]);
+        }
+    }
+    // over the warp's four row groups, then over the warps in order
+#pragma unroll
+    for (int t = 0; t < NC; ++t) {
+        float* a = &ak[t].x;
+        float* b = &av[t].x;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int o = kLanesPerRow; o < 32; o <<= 1) {
+                a[c] += __shfl_xor_sync(0xffffffffu, a[c], o);
+                b[c] += __shfl_xor_sync(0xffffffffu, b[c], o);
+            }
+            if ((threadIdx.x & 31) < kLanesPerRow) {
+                part[warp][0][4 * (r8 + kLanesPerRow * t) + c] = a[c];
+                part[warp][1][4 * (r8 + kLanesPerRow * t) + c] = b[c];
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * hd; e += kBwdThreads) {
+        const int which = e / hd, d = e % hd;
+        float* to = (which ? dv : dk) + krow + d;
+        float sum = *to;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += part[w][which][d];
+        *to = sum;
+    }
+}
+
+template <int HP>
+void launch_far(const AttnProblem& p, const void* dout, const float* dsum, void* dk, void* dv, cudaStream_t stream) {
+    attn_bwd_far_kernel<HP><<<dim3(p.batch, p.kv_heads, p.sinks), kBwdThreads, 0, stream>>>(
+        p, static_cast<const float*>(dout), dsum, static_cast<float*>(dk), static_cast<float*>(dv));
 }
 
 // D_i = dO_i . O_i for every row (slot, head) of the slot view: 8 lanes per row, VEC elements per
@@ -449,10 +545,15 @@ cudaError_t launch_attn_bwd(const AttnProblem& p, const void* dout, const float*
                             void* dk, void* dv, int is_bf16, cudaStream_t stream) {
     const int64_t slots = static_cast<int64_t>(p.total_tokens) * p.slot_mult;
     if (slots == 0) return cudaSuccess;
-    if (p.head_dim > 128) return cudaErrorInvalidValue;
+    if (p.head_dim > 128 || (p.sinks > 0 && is_bf16)) return cudaErrorInvalidValue;
     const unsigned tiles = static_cast<unsigned>((slots + kRowsPerBlock - 1) / kRowsPerBlock);
     if (is_bf16) launch_bwd_t<__nv_bfloat16>(p, dout, dsum, dq, dk, dv, tiles, stream);
     else launch_bwd_t<float>(p, dout, dsum, dq, dk, dv, tiles, stream);
+    if (p.sinks > 0 && p.window > 0) {
+        if (p.head_dim <= 32) launch_far<32>(p, dout, dsum, dk, dv, stream);
+        else if (p.head_dim <= 64) launch_far<64>(p, dout, dsum, dk, dv, stream);
+        else launch_far<128>(p, dout, dsum, dk, dv, stream);
+    }
     return cudaGetLastError();
 }
 

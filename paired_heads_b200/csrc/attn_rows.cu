@@ -27,7 +27,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bf
 
 template <bool PAGED>
 __global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(GatherProblem p) {
-    __shared__ float qs[kRowWarps][kMaxDim];
+    __shared__ __align__(16) float qs[kRowWarps][kMaxDim];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t rows = static_cast<int64_t>(p.total_q) * p.mult * p.heads;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
@@ -76,7 +76,21 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(GatherProblem
             }
             const float* k = kb + kr * stride;
             float dot = 0.f;
-            for (int d = 0; d < D; ++d) dot = fmaf(qs[warp][d], k[d], dot);
+            if (D % 4 == 0) {  // rows are 16-byte aligned
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int d = 0; d < D; d += 4) {
+                    const float4 k4 = __ldg(reinterpret_cast<const float4*>(k + d));
+                    const float4 q4 = *reinterpret_cast<const float4*>(&qs[warp][d]);
+                    part[0] = fmaf(q4.x, k4.x, part[0]);
+                    part[1] = fmaf(q4.y, k4.y, part[1]);
+                    part[2] = fmaf(q4.z, k4.z, part[2]);
+                    part[3] = fmaf(q4.w, k4.w, part[3]);
+                }
+                dot = (part[0] + part[1]) + (part[2] + part[3]);
+            } else {
+                for (int d = 0; d < D; ++d) dot = fmaf(qs[warp][d], k[d], dot);
+            }
             x = dot * scale2;
         }
         float mx = x;
@@ -93,6 +107,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(GatherProblem
 #pragma unroll
         for (int t = 0; t < kMaxDim / 32; ++t) acc[t] *= alpha;
         const int n = c1 - c < 32 ? c1 - c : 32;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, j);
             const float* v = vb + __shfl_sync(0xffffffffu, kr, j) * stride;
