@@ -396,68 +396,79 @@ def pha_attn_status(workspace, stream=None):
 # call is made on the tensor's device.
 
 _torch = None
+_raw_stream = None
 
 
 def _lazy_torch():
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
 
+        # (building a torch Stream object to ask for its handle takes 3 us of every call)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
         _torch = torch
     return _torch
 
 
-def _want(name, t, dtype, *shape):
-    """t is a contiguous tensor of this dtype and shape."""
+def _explain(fn, index, name, t, dtype, shape):
+    """Raises what is wrong with a tensor that _run found wanting."""
     if t.dtype is not dtype:
-        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+        raise TypeError(f"{fn}: {name}: {t.dtype}, expected {dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        raise ValueError(f"{fn}: {name}: shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
+        raise ValueError(f"{fn}: {name}: not contiguous")
+    raise ValueError(f"{fn}: {name}: on {t.device}, others on device {index}")
 
 
-def _run(fn, args, stream, first, *others):
-    """Calls the library on the device of `first`, which the other tensors must share."""
-    cuda = _lazy_torch().cuda
-    index = first.get_device()
+def _run(fn, wanted, args, stream):
+    """Calls the library. wanted: (name, tensor, dtype, shape) of each tensor argument (the first one's
+    device is everybody's); None for one that is left out."""
+    index = wanted[0][1].get_device()
+    for w in wanted:
+        if w is not None:
+            t = w[1]
+            if (t.dtype is not w[2] or t.shape != w[3] or not t.is_contiguous()
+                    or t.get_device() != index):
+                _explain(fn, index, *w)
     if index < 0:
         raise ValueError(f"{fn}: tensors not on a CUDA device")
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
-    call = getattr(_lib, fn)
+    cuda = _lazy_torch().cuda
     if cuda.current_device() != index:
         with cuda.device(index):
-            return _check(fn, call(*args, _stream(stream, first)))
+            return _check(fn, getattr(_lib, fn)(*args, _stream(stream, wanted[0][1])))
     if stream is None:
-        stream = cuda.current_stream().cuda_stream
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    rc = call(*args, stream)
+    rc = getattr(_lib, fn)(*args, stream)
     if rc != 0:
         _check(fn, rc)
+
+
+def _scratch(workspace):
+    """What _run wants of a workspace: contiguous bytes of any type and shape, on the device."""
+    return ("workspace", workspace, workspace.dtype, workspace.shape)
+
+
+def _status(status):
+    return None if status is None else ("status", status, _int32(), (1,))
 
 
 def _int32():
     return _lazy_torch().int32
 
 
-def _attn_shape(q, k, o, lse):
-    """Checks q, o, lse of a call; (tokens, heads, kv heads, head_dim, dtype code)."""
-    torch = _lazy_torch()
-    dt = PHA_BF16 if q.dtype is torch.bfloat16 else _dtype_code(q)
+def _dims(q, k):
+    """(tokens, heads, kv heads, head_dim, dtype, dtype code) of a call."""
+    dt = q.dtype
     t, h, hd = q.shape
-    hkv = k.shape[-2]
-    _want("q", q, q.dtype, t, h, hd)
-    _want("o", o, q.dtype, t, h, hd)
-    if lse is not None:
-        _want("lse", lse, torch.float32, t, h)
-    return t, h, hkv, hd, dt
+    return t, h, k.shape[-2], hd, dt, PHA_BF16 if dt is _lazy_torch().bfloat16 else _dtype_code(q)
 
 
 def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def pha_attn_sinks_workspace_bytes(batch: int, max_len: int, n_heads: int, n_kv_heads: int,
@@ -479,30 +490,33 @@ def pha_attn_sinks_fwd(q, k, v, cu_seqlens, max_len: int, o, lse, workspace, *, 
                        sinks: int, paired: bool = False, scale: float = 0.0, stream=None):
     """Causal varlen attention with a sliding window and `sinks` visible first slots per document,
     into o (like q) and lse [T][H] float32 (or None). pha_attn_status(workspace) reports."""
-    t, h, hkv, hd, dt = _attn_shape(q, k, o, lse)
-    _want("k", k, q.dtype, t, hkv, hd)
-    _want("v", v, q.dtype, t, hkv, hd)
-    _want("cu_seqlens", cu_seqlens, _int32(), cu_seqlens.shape[0])
+    t, h, hkv, hd, dt, code = _dims(q, k)
+    n = cu_seqlens.shape[0]
     _run("pha_attn_sinks_fwd",
-         (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
-          max_len, t, h, hkv, hd, dt, window, sinks, int(paired), scale, o.data_ptr(), _ptr(lse),
-          workspace.data_ptr(), _nbytes(workspace)), stream, q, k, v, cu_seqlens, o, lse, workspace)
+         (("q", q, dt, (t, h, hd)), ("k", k, dt, (t, hkv, hd)), ("v", v, dt, (t, hkv, hd)),
+          ("cu_seqlens", cu_seqlens, _int32(), (n,)), ("o", o, dt, (t, h, hd)),
+          None if lse is None else ("lse", lse, _torch.float32, (t, h)), _scratch(workspace)),
+         (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), n - 1, max_len, t, h,
+          hkv, hd, code, window, sinks, paired, scale, o.data_ptr(), _ptr(lse),
+          workspace.data_ptr(), _nbytes(workspace)), stream)
 
 
 def pha_attn_sinks_bwd(q, k, v, o, lse, dout, cu_seqlens, max_len: int, dq, dk, dv, workspace, *,
                        window: int, sinks: int, paired: bool = False, scale: float = 0.0,
                        stream=None):
     """Backward of pha_attn_sinks_fwd (o, lse: its outputs): dq, dk, dv for dout."""
-    t, h, hkv, hd, dt = _attn_shape(q, k, o, lse)
-    for name, x, heads in (("k", k, hkv), ("v", v, hkv), ("dout", dout, h), ("dq", dq, h),
-                           ("dk", dk, hkv), ("dv", dv, hkv)):
-        _want(name, x, q.dtype, t, heads, hd)
-    _want("cu_seqlens", cu_seqlens, _int32(), cu_seqlens.shape[0])
+    t, h, hkv, hd, dt, code = _dims(q, k)
+    n = cu_seqlens.shape[0]
+    like_q, like_k = (t, h, hd), (t, hkv, hd)
     _run("pha_attn_sinks_bwd",
-         (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), dout.data_ptr(),
-          cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, max_len, t, h, hkv, hd, dt, window, sinks,
-          int(paired), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-          _nbytes(workspace)), stream, q, k, v, o, lse, dout, cu_seqlens, dq, dk, dv, workspace)
+         (("q", q, dt, like_q), ("k", k, dt, like_k), ("v", v, dt, like_k), ("o", o, dt, like_q),
+          ("lse", lse, _torch.float32, (t, h)), ("dout", dout, dt, like_q), ("dq", dq, dt, like_q),
+          ("dk", dk, dt, like_k), ("dv", dv, dt, like_k),
+          ("cu_seqlens", cu_seqlens, _int32(), (n,)), _scratch(workspace)),
+         (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+          cu_seqlens.data_ptr(), n - 1, max_len, t, h, hkv, hd, code, window, sinks, paired, scale,
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), _nbytes(workspace)),
+         stream)
 
 
 def pha_attn_paged_workspace_bytes(batch: int, max_q: int, max_kv: int, total_q: int, n_heads: int,
@@ -523,131 +537,119 @@ def pha_attn_paged_fwd(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, max
     """Attention of each sequence's new tokens q over its paged cache (k_pages, v_pages
     [pages][page_size][Hkv][hd], page_table [batch][max_pages], kv_lens [batch] with the new tokens
     included) into o and lse (or None). status: int32[1], raised on bad lengths or pages."""
-    t, h, hkv, hd, dt = _attn_shape(q, k_pages, o, lse)
-    n_pages, page = k_pages.shape[:2]
-    batch = cu_seqlens.shape[0] - 1
-    _want("k_pages", k_pages, q.dtype, n_pages, page, hkv, hd)
-    _want("v_pages", v_pages, q.dtype, n_pages, page, hkv, hd)
+    t, h, hkv, hd, dt, code = _dims(q, k_pages)
+    pool = k_pages.shape
+    n_pages, page = pool[0], pool[1]
+    batch, max_pages = page_table.shape
     i32 = _int32()
-    max_pages = page_table.shape[-1]
-    _want("page_table", page_table, i32, batch, max_pages)
-    _want("cu_seqlens", cu_seqlens, i32, batch + 1)
-    _want("kv_lens", kv_lens, i32, batch)
-    if status is not None:
-        _want("status", status, i32, 1)
     _run("pha_attn_paged_fwd",
-         (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-          max_pages, n_pages, page, cu_seqlens.data_ptr(), kv_lens.data_ptr(), batch,
-          max_q, max_kv, t, h, hkv, hd, dt, window, sinks, int(paired), scale, o.data_ptr(),
-          _ptr(lse), workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream, q, k_pages,
-         v_pages, page_table, cu_seqlens, kv_lens, o, lse, workspace, status)
+         (("q", q, dt, (t, h, hd)), ("k_pages", k_pages, dt, (n_pages, page, hkv, hd)),
+          ("v_pages", v_pages, dt, pool), ("page_table", page_table, i32, (batch, max_pages)),
+          ("cu_seqlens", cu_seqlens, i32, (batch + 1,)), ("kv_lens", kv_lens, i32, (batch,)),
+          ("o", o, dt, (t, h, hd)),
+          None if lse is None else ("lse", lse, _torch.float32, (t, h)), _scratch(workspace),
+          _status(status)),
+         (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), max_pages,
+          n_pages, page, cu_seqlens.data_ptr(), kv_lens.data_ptr(), batch, max_q, max_kv, t, h,
+          hkv, hd, code, window, sinks, paired, scale, o.data_ptr(), _ptr(lse),
+          workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream)
 
 
 def pha_cache_append(k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, *, status=None,
                      stream=None):
     """Writes the new tokens' k, v [T][Hkv][hd] to their places in k_pages, v_pages (one layer)."""
-    t, hkv, hd = k.shape
-    n_pages, page = k_pages.shape[:2]
-    batch = cu_seqlens.shape[0] - 1
-    _want("k", k, k.dtype, t, hkv, hd)
-    _want("v", v, k.dtype, t, hkv, hd)
-    _want("k_pages", k_pages, k.dtype, n_pages, page, hkv, hd)
-    _want("v_pages", v_pages, k.dtype, n_pages, page, hkv, hd)
+    shape, dt = k.shape, k.dtype
+    t, hkv, hd = shape
+    pool = k_pages.shape
+    n_pages, page = pool[0], pool[1]
+    batch, max_pages = page_table.shape
     i32 = _int32()
-    max_pages = page_table.shape[-1]
-    _want("page_table", page_table, i32, batch, max_pages)
-    _want("cu_seqlens", cu_seqlens, i32, batch + 1)
-    _want("kv_lens", kv_lens, i32, batch)
-    if status is not None:
-        _want("status", status, i32, 1)
     _run("pha_cache_append",
+         (("k", k, dt, shape), ("v", v, dt, shape), ("k_pages", k_pages, dt, (n_pages, page, hkv, hd)),
+          ("v_pages", v_pages, dt, pool), ("page_table", page_table, i32, (batch, max_pages)),
+          ("cu_seqlens", cu_seqlens, i32, (batch + 1,)), ("kv_lens", kv_lens, i32, (batch,)),
+          _status(status)),
          (k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           page_table.data_ptr(), max_pages, n_pages, page, cu_seqlens.data_ptr(),
-          kv_lens.data_ptr(), batch, t, hkv, hd, k.element_size(), _ptr(status)), stream, k, v,
-         k_pages, v_pages, page_table, cu_seqlens, kv_lens, status)
+          kv_lens.data_ptr(), batch, t, hkv, hd, k.element_size(), _ptr(status)), stream)
 
 
 def pha_cache_workspace_bytes(n_pages: int, n_seqs: int) -> int:
     return int(_lib.pha_cache_workspace_bytes(n_pages, n_seqs))
 
 
-def _cache_state(page_table, kv_lens, page_refs, status):
-    """Checks the bookkeeping tensors; (max_pages, sequences, pages)."""
+def _cache_tensors(page_table, kv_lens, page_refs, status):
+    """What _run wants of the bookkeeping tensors; (max_pages, sequences, pages)."""
     i32 = _int32()
-    n_seqs, max_pages = page_table.shape
-    _want("page_table", page_table, i32, n_seqs, max_pages)
-    if kv_lens is not None:
-        _want("kv_lens", kv_lens, i32, n_seqs)
-    _want("page_refs", page_refs, i32, page_refs.shape[0])
-    if status is not None:
-        _want("status", status, i32, 1)
-    return max_pages, n_seqs, page_refs.shape[0]
+    shape = page_table.shape
+    n_seqs, max_pages = shape
+    n_pages = page_refs.shape[0]
+    wanted = (("page_table", page_table, i32, shape),
+              None if kv_lens is None else ("kv_lens", kv_lens, i32, (n_seqs,)),
+              ("page_refs", page_refs, i32, (n_pages,)), _status(status))
+    return wanted, max_pages, n_seqs, n_pages
 
 
 def _cache_pools(k_cache, v_cache, n_pages):
-    """Checks pools [layers][pages][page_size][Hkv][hd]; (layers, bytes of one page)."""
-    layers, _, page, hkv, hd = k_cache.shape
-    _want("k_cache", k_cache, k_cache.dtype, layers, n_pages, page, hkv, hd)
-    _want("v_cache", v_cache, k_cache.dtype, layers, n_pages, page, hkv, hd)
-    return layers, page * hkv * hd * k_cache.element_size()
+    """The same of pools [layers][pages][page_size][Hkv][hd]; (layers, bytes of one page)."""
+    shape, dt = k_cache.shape, k_cache.dtype
+    layers, _, page, hkv, hd = shape
+    wanted = (("k_cache", k_cache, dt, (layers, n_pages, page, hkv, hd)), ("v_cache", v_cache, dt, shape))
+    return wanted, layers, page * hkv * hd * k_cache.element_size()
 
 
 def pha_cache_fork(page_table, kv_lens, page_refs, src, dst, workspace, *, status=None,
                    stream=None):
     """Empty sequences dst[i] become further holders of src[i]'s pages (nothing is copied)."""
-    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
-    n = src.shape[0]
-    _want("src", src, _int32(), n)
-    _want("dst", dst, _int32(), n)
+    wanted, mp, ns, npg = _cache_tensors(page_table, kv_lens, page_refs, status)
+    n, i32 = src.shape[0], _int32()
     _run("pha_cache_fork",
+         wanted + (("src", src, i32, (n,)), ("dst", dst, i32, (n,)), _scratch(workspace)),
          (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg,
           src.data_ptr(), dst.data_ptr(), n, workspace.data_ptr(), _nbytes(workspace),
-          _ptr(status)), stream, page_table, kv_lens, page_refs, src, dst, workspace, status)
+          _ptr(status)), stream)
 
 
 def pha_cache_reserve(page_table, kv_lens, page_refs, seqs, new_tokens, k_cache, v_cache, workspace,
                       *, status=None, stream=None):
     """Room for new_tokens[i] more tokens of sequence seqs[i]; a shared last page that a sequence
     grows into is copied (k_cache, v_cache [layers][pages][page_size][Hkv][hd])."""
-    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
-    layers, page_bytes = _cache_pools(k_cache, v_cache, npg)
-    n = seqs.shape[0]
-    _want("seqs", seqs, _int32(), n)
-    _want("new_tokens", new_tokens, _int32(), n)
+    wanted, mp, ns, npg = _cache_tensors(page_table, kv_lens, page_refs, status)
+    pools, layers, page_bytes = _cache_pools(k_cache, v_cache, npg)
+    n, i32 = seqs.shape[0], _int32()
     _run("pha_cache_reserve",
+         wanted + pools + (("seqs", seqs, i32, (n,)), ("new_tokens", new_tokens, i32, (n,)),
+                           _scratch(workspace)),
          (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg,
           k_cache.shape[2], seqs.data_ptr(), new_tokens.data_ptr(), n, k_cache.data_ptr(),
           v_cache.data_ptr(), layers, page_bytes, workspace.data_ptr(), _nbytes(workspace),
-          _ptr(status)), stream, page_table, kv_lens, page_refs, seqs, new_tokens, k_cache,
-         v_cache, workspace, status)
+          _ptr(status)), stream)
 
 
 def pha_cache_free(page_table, kv_lens, page_refs, seqs, workspace, *, status=None, stream=None):
     """Sequences seqs[i] let go of their pages and become empty."""
-    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
+    wanted, mp, ns, npg = _cache_tensors(page_table, kv_lens, page_refs, status)
     n = seqs.shape[0]
-    _want("seqs", seqs, _int32(), n)
-    _run("pha_cache_free",
+    _run("pha_cache_free", wanted + (("seqs", seqs, _int32(), (n,)), _scratch(workspace)),
          (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg,
-          seqs.data_ptr(), n, workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream,
-         page_table, kv_lens, page_refs, seqs, workspace, status)
+          seqs.data_ptr(), n, workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream)
 
 
 def pha_cache_trim(page_table, kv_lens, page_refs, page_size: int, *, window: int, sinks: int = 0,
                    paired: bool = False, status=None, stream=None):
     """Every sequence lets go of the pages that no later token sees with this window and sinks."""
-    mp, ns, npg = _cache_state(page_table, kv_lens, page_refs, status)
-    _run("pha_cache_trim",
+    wanted, mp, ns, npg = _cache_tensors(page_table, kv_lens, page_refs, status)
+    _run("pha_cache_trim", wanted,
          (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg, page_size,
-          window, sinks, int(paired), _ptr(status)), stream, page_table, kv_lens, page_refs, status)
+          window, sinks, paired, _ptr(status)), stream)
 
 
 def pha_cache_compact(page_table, page_refs, k_cache, v_cache, workspace, *, status=None,
                       stream=None):
     """Moves the pages in use together at the front of the pool, in all layers."""
-    mp, ns, npg = _cache_state(page_table, None, page_refs, status)
-    layers, page_bytes = _cache_pools(k_cache, v_cache, npg)
-    _run("pha_cache_compact",
+    wanted, mp, ns, npg = _cache_tensors(page_table, None, page_refs, status)
+    pools, layers, page_bytes = _cache_pools(k_cache, v_cache, npg)
+    _run("pha_cache_compact", wanted + pools + (_scratch(workspace),),
          (page_table.data_ptr(), mp, ns, page_refs.data_ptr(), npg, k_cache.data_ptr(),
           v_cache.data_ptr(), layers, page_bytes, workspace.data_ptr(), _nbytes(workspace),
-          _ptr(status)), stream, page_table, page_refs, k_cache, v_cache, workspace, status)
+          _ptr(status)), stream)
