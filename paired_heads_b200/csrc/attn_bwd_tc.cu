@@ -412,6 +412,9 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idesc1 = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
             constexpr uint32_t idesc2 = idesc_bf16_f32(kBlockM, HD, 0, 1);
+            // columns of a step over the sinks alone (whole K = 16 slices)
+            const int sink_cols = SINK ? (p.sinks + 15) & ~15 : 0;
+            const uint32_t idesc_sink = (idesc1 & ~(0x3Fu << 17)) | (static_cast<uint32_t>(sink_cols >> 3) << 17);
             const uint32_t tm_s = tmem + L::kTmS, tm_dp = tmem + L::kTmDP;
             const uint32_t tm_acc_p = tmem + L::kTmAcc;                         // dV
             const uint32_t tm_acc_ds = tmem + L::kTmAcc + (KEYMAJOR ? HD : 0);  // dK or dQ
@@ -448,11 +451,14 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                                 ok = false;
                         if (!ok) break;
                         tc_fence_after();
+                        // a step over the sinks alone takes the first sink_cols columns only
+                        const bool sink_step = SINK && !KEYMAJOR && o.sink0 && s == 0;
+                        const uint32_t id1 = sink_step ? idesc_sink : idesc1;
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk) {
-                            umma_f16_ss(tm_s, desc_kmajor(x0, kk), desc_kmajor(y0, kk), idesc1,
+                            umma_f16_ss(tm_s, desc_kmajor(x0, kk), desc_kmajor(y0, kk), id1,
                                         kk == 0 ? 0u : 1u);
-                            umma_f16_ss(tm_dp, desc_kmajor(x1, kk), desc_kmajor(y1, kk), idesc1,
+                            umma_f16_ss(tm_dp, desc_kmajor(x1, kk), desc_kmajor(y1, kk), id1,
                                         kk == 0 ? 0u : 1u);
                         }
                         umma_commit(&bars->s_full[0]);  // one per elementwise warpgroup
@@ -471,6 +477,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
                                 const uint32_t acc = (s > 0 || h > 0 || kk > 0) ? 1u : 0u;
+                                if (SINK && !KEYMAJOR && sink_step && 64 * h + 16 * kk >= sink_cols) continue;
                                 umma_f16_ts(tm_acc_ds, tm_dp + 64 * h + 8 * kk, desc_v(y0, 4 * h + kk),
                                             idesc2, acc);
                                 if (KEYMAJOR)
@@ -560,6 +567,11 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                                                                dev_status));
                         if (!ok) break;
                         tc_fence_after();
+                        // what nobody reads is left out: columns behind the sinks' slices in a step over
+                        // them alone, rows that are no sinks in a far piece (their sums are not kept)
+                        const int n_cols = SINK && !KEYMAJOR && o.sink0 && s == 0 ? (p.sinks + 15) & ~15 : kBlockN;
+                        const bool idle = SINK && (64 * h >= n_cols || (KEYMAJOR && o.piece >= 0 && r0 >= p.sinks));
+                        if (!idle) {
                         // the half's 64 columns of S and dP, one wait
                         uint32_t sv[64], dv[64];
 #pragma unroll
@@ -576,6 +588,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
 #pragma unroll
                         for (int cc = 0; cc < 2; ++cc) {
                             const int c = 2 * h + cc;
+                            if (SINK && 32 * c >= n_cols) continue;
                             uint32_t pk[16], dk[16];
                             // SINK: bit e = column 32 c + e is visible
                             const uint32_t bits = SINK ? low_bits(c_hi + 1 - 32 * c) &
@@ -616,6 +629,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                             // columns of this half already read
                             if (KEYMAJOR) tmem_st16(tm_lane + L::kTmS + 16 * c + 32 * h, pk);
                             tmem_st16(tm_lane + L::kTmDP + 16 * c + 32 * h, dk);
+                        }
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -772,8 +786,8 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, L::kTmemCols);
 }
 
-// Block (document, kv head): the sinks' rows of dk, dv of documents with far query tiles, summed over
-// the window's part and the pieces in order.
+// Block (document, kv head, 256 of the values): the sinks' rows of dk, dv of documents with far query
+// tiles, summed over the window's part and the pieces in order.
 __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProblem p, __nv_bfloat16* dk,
                                                                 __nv_bfloat16* dv, const WorkspaceHeader* hdr) {
     if (hdr->status != DEV_OK) return;
@@ -792,7 +806,8 @@ __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProble
     const int64_t stride = static_cast<int64_t>(p.kv_heads) * width;
     const float* first = p.sink_part + (static_cast<int64_t>(d) * p.kv_heads + g) * width;
     const float* rest = p.sink_part + (place * p.kv_heads + g) * width;
-    for (int x = threadIdx.x; x < width; x += 256) {
+    const int x = blockIdx.z * 256 + threadIdx.x;
+    if (x < width) {
         float sum = first[x];
 #pragma unroll 8
         for (int f = 0; f < pieces; ++f) sum += rest[f * stride + x];
@@ -873,7 +888,7 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
 
 cudaError_t launch_attn_bwd_sink_sum(const AttnProblem& p, void* dk, void* dv,
                                      const WorkspaceHeader* hdr, cudaStream_t stream) {
-    attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads), 256, 0, stream>>>(
+    attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads, (p.sinks * 2 * p.head_dim + 255) / 256), 256, 0, stream>>>(
         p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr);
     return cudaGetLastError();
 }

@@ -17,11 +17,13 @@ namespace pha {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanNear = 2048;  // sequences whose tile counts are kept in shared memory
+constexpr int kPlanNear = 2048;        // sequences whose tile counts are kept in shared memory
+constexpr int kPlanNearSteps = 3000;   // row tiles whose steps are
 
 __global__ void __launch_bounds__(kPlanThreads) gather_plan_kernel(GatherProblem p, int64_t max_tiles,
                                                                    int* __restrict__ before_far,
-                                                                   int64_t* __restrict__ steps, int strict) {
+                                                                   int64_t* __restrict__ steps_far, int strict) {
+    __shared__ int64_t near_steps[kPlanNearSteps + 1];
     __shared__ int64_t sums[kPlanThreads / 32];
     __shared__ int near[kPlanNear];
     __shared__ int bad;
@@ -55,6 +57,7 @@ __global__ void __launch_bounds__(kPlanThreads) gather_plan_kernel(GatherProblem
     }
     if (max_tiles == 0) return;
     const int chunks = p.heads / p.pack;
+    int64_t* steps = n_tiles <= kPlanNearSteps ? near_steps : steps_far;
     int64_t total = 0;
     if (code == DEV_OK) {
         for (int64_t base = 0; base < n_tiles; base += kPlanThreads) {

@@ -57,11 +57,12 @@ FwdPlan fwd_plan(int batch, int max_len, int n_heads, int n_kv_heads, int head_d
     return w;
 }
 
-// Backward: header, per-document scratch and the largest work list (key tiles and far pieces), then
-// D, then the far pieces' partial sums.
+// Backward: header, per-document scratch and work list of the query tiles, the same of the key tiles
+// (with far pieces; apart, so that a later call over the same documents keeps both lists), D, the far
+// pieces' partial sums.
 struct BwdPlan {
-    int64_t items;
-    size_t list, dsum, part, bytes;
+    int64_t items_q, items_k;
+    size_t list, keys, dsum, part, bytes;  // list: of a work list behind its header
 };
 
 BwdPlan bwd_plan(int batch, int max_len, int total_tokens, int n_heads, int n_kv_heads, int head_dim,
@@ -73,9 +74,11 @@ BwdPlan bwd_plan(int batch, int max_len, int total_tokens, int n_heads, int n_kv
     const int piece = far ? sink_piece_tiles(window, max_len, mult) : 1;
     const int64_t pieces = far ? (tiles + piece - 1) / piece : 0;
     BwdPlan w{};
-    w.items = static_cast<int64_t>(batch) * (tiles + pieces) * (n_heads / mult);
+    w.items_q = static_cast<int64_t>(batch) * tiles * (n_heads / mult);
+    w.items_k = static_cast<int64_t>(batch) * (tiles + pieces) * (n_heads / mult);
     w.list = kWorkspaceHeaderBytes + workspace_doc_bytes(batch);
-    w.dsum = w.list + padded(sizeof(int4) * static_cast<size_t>(w.items));
+    w.keys = padded(w.list + sizeof(int4) * static_cast<size_t>(w.items_q));
+    w.dsum = w.keys + padded(w.list + sizeof(int4) * static_cast<size_t>(w.items_k));
     w.part = w.dsum + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
     const int64_t slots = static_cast<int64_t>(total_tokens) * mult;
     w.bytes = w.part + (far ? padded(sizeof(float) * static_cast<size_t>(sink_part_slots(batch, slots, piece)) *
@@ -204,15 +207,19 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
     const BwdPlan w = bwd_plan(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, window, sinks, paired);
     auto* base = static_cast<uint8_t*>(workspace);
     auto* hdr = reinterpret_cast<WorkspaceHeader*>(base);
-    auto* docs = reinterpret_cast<int*>(base + kWorkspaceHeaderBytes);
-    auto* items = reinterpret_cast<int4*>(base + w.list);
+    auto* hdr_k = reinterpret_cast<WorkspaceHeader*>(base + w.keys);
+    auto list = [&](size_t at) { return reinterpret_cast<int4*>(base + at + w.list); };
+    auto build = [&](ScheduleMode mode, size_t at, int64_t items) {
+        return launch_schedule(p, mode, items < INT32_MAX ? static_cast<int>(items) : INT32_MAX,
+                               reinterpret_cast<int*>(base + at + kWorkspaceHeaderBytes), list(at),
+                               reinterpret_cast<WorkspaceHeader*>(base + at), stream);
+    };
     float* dsum = reinterpret_cast<float*>(base + w.dsum);
     p.sink_part = reinterpret_cast<float*>(base + w.part);
     p.checked = hdr;
-    const int capacity = w.items < INT32_MAX ? static_cast<int>(w.items) : INT32_MAX;
     const bool tc = dtype == PHA_BF16;
     // the scheduler also checks cu_seqlens; without a list to walk (CUDA cores) only that is used
-    if (launch_schedule(p, kSchedTilesQ, capacity, docs, items, hdr, stream) != cudaSuccess ||
+    if (build(kSchedTilesQ, 0, w.items_q) != cudaSuccess ||
         launch_attn_bwd_dsum(p, o, dout, dsum, tc, stream) != cudaSuccess)
         return PHA_ERR_CUDA;
     if (!tc) return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, 0, stream));
@@ -225,11 +232,11 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
         !encode_slot_map(&tdv, dv, wk, rows, 16))
         return PHA_ERR_CUDA;
     if (launch_attn_bwd_zero_outside(p, dq, dk, dv, stream) != cudaSuccess ||
-        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, items, hdr, 1, stream, true) !=
+        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, list(0), hdr, 1, stream, true) !=
             cudaSuccess ||
-        launch_schedule(p, kSchedTilesK, capacity, docs, items, hdr, stream) != cudaSuccess ||
-        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, items, hdr, 2, stream, true) !=
-            cudaSuccess)
+        build(kSchedTilesK, w.keys, w.items_k) != cudaSuccess ||
+        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, list(w.keys), hdr_k, 2, stream,
+                           true) != cudaSuccess)
         return PHA_ERR_CUDA;
     return p.sinks > 0 ? of(launch_attn_bwd_sink_sum(p, dk, dv, hdr, stream)) : PHA_OK;
 }
