@@ -291,8 +291,9 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
 
     const int n_items = *reinterpret_cast<volatile int*>(&hdr->n_items);
     const int H = p.heads, Hkv = p.kv_heads, G = H / Hkv;
-    static_assert(8 * kTcRegsSoftmax + 4 * kTcRegsOther <= 12 * 168, "register split");
-    if (warp >= 8) regs_decrease<kTcRegsOther>();  // the whole third warpgroup, then its roles
+    constexpr int kRegsOther = SINK ? 104 : kTcRegsOther;  // (the staggered issue holds more)
+    static_assert(8 * kTcRegsSoftmax + 4 * kRegsOther <= 12 * 168, "register split");
+    if (warp >= 8) regs_decrease<kRegsOther>();  // the whole third warpgroup, then its roles
     const bool reuse = !GEN && (!KEYMAJOR || G == 1);
     // X = (K, V) and Y = (Q, dO) (key-major), or the other way round
     const CUtensorMap* mx0 = KEYMAJOR ? &tm_k : &tm_q;
@@ -412,9 +413,6 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idesc1 = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
             constexpr uint32_t idesc2 = idesc_bf16_f32(kBlockM, HD, 0, 1);
-            // columns of a step over the sinks alone (whole K = 16 slices)
-            const int sink_cols = SINK ? (p.sinks + 15) & ~15 : 0;
-            const uint32_t idesc_sink = (idesc1 & ~(0x3Fu << 17)) | (static_cast<uint32_t>(sink_cols >> 3) << 17);
             const uint32_t tm_s = tmem + L::kTmS, tm_dp = tmem + L::kTmDP;
             const uint32_t tm_acc_p = tmem + L::kTmAcc;                         // dV
             const uint32_t tm_acc_ds = tmem + L::kTmAcc + (KEYMAJOR ? HD : 0);  // dK or dQ
@@ -423,75 +421,154 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
             FillTrack<KEYMAJOR> ft;
             bool ok = true;
             ItemWalk wk;
-            for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
-                if (!wk.has()) continue;
-                const BandItem it = decode_band(wk.cur);
-                if (!item_used<KEYMAJOR>(it, G)) continue;
-                for (int u = 0; ok && u < (SINK ? 1 : it.n_qt); ++u) {
-                    const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, u, G, p);
-                    if (!mbar_wait(&bars->x_full, oc & 1, abort_flag, dev_status)) {
-                        ok = false;
-                        break;
+            if constexpr (SINK) {
+                // The two halves of a step run half a step apart, each with its own S and dP products (N =
+                // 64): while one warpgroup is at its elementwise work the other half's products run.
+                // (Both halves at once, as below, leave the tensor cores idle meanwhile: dQ 675, dK / dV 798
+                // us against 548 and 643 for 2 x 8192 tokens, 32 / 8 heads of 128, window 1024.)
+                uint32_t n[2] = {0, 0};  // steps of half h whose S and dP products are issued
+                struct Second {          // the second products of half 1 still to issue
+                    bool on, first, last;
+                    uint32_t st, cols;
+                } later{false, false, false, 0, 0};
+                constexpr int kHalf = kBlockN / 2;
+                auto first_products = [&](int h, uint32_t st, uint32_t cols) {
+                    if (n[h] > 0)
+                        ok = mbar_wait(&bars->m2_done[h], (n[h] - 1) & 1, abort_flag, dev_status);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile + h * kHalf * 128, y1 = y0 + L::kTile;
+                    const uint32_t id = (idesc1 & ~(0x3Fu << 17)) | ((cols >> 3) << 17);
+                    const uint64_t dx0 = desc_kmajor(x0, 0), dx1 = desc_kmajor(x1, 0);
+                    const uint64_t dy0 = desc_kmajor(y0, 0), dy1 = desc_kmajor(y1, 0);
+                    if (cols > 0)
+#pragma unroll
+                        for (int kk = 0; kk < HD / 16; ++kk) {  // (as desc_kmajor steps)
+                            const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            umma_f16_ss(tm_s + kHalf * h, dx0 + step, dy0 + step, id, kk == 0 ? 0u : 1u);
+                            umma_f16_ss(tm_dp + kHalf * h, dx1 + step, dy1 + step, id, kk == 0 ? 0u : 1u);
+                        }
+                    umma_commit(&bars->s_full[h]);
+                    ++n[h];
+                };
+                auto second_products = [&](int h, uint32_t st, uint32_t cols, bool first) {
+                    ok = mbar_wait(&bars->p_full[h], (n[h] - 1) & 1, abort_flag, dev_status);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile, y1 = y0 + L::kTile;
+                    const uint64_t dy0 = desc_v(y0, 4 * h), dy1 = desc_v(y1, 4 * h);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t acc = (!first || h > 0 || kk > 0) ? 1u : 0u;
+                        if (static_cast<uint32_t>(16 * kk) >= cols) continue;
+                        umma_f16_ts(tm_acc_ds, tm_dp + kHalf * h + 8 * kk, dy0 + kk * (2048 >> 4), idesc2, acc);
+                        if (KEYMAJOR)
+                            umma_f16_ts(tm_acc_p, tm_s + kHalf * h + 8 * kk, dy1 + kk * (2048 >> 4), idesc2, acc);
                     }
-                    for (int s = 0; s < o.n_sub; ++s) {
-                        const StepFill f = ft.step(reuse, u, it.n_qt, s, o.n_sub);
-                        const uint32_t st = f.idx & 1;
-                        const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile, y1 = y0 + L::kTile;
-                        // each fill is waited for once, by its first reader, in fill order
-                        if (f.first && !mbar_wait(SINK ? &bars->y_ok[st] : &bars->y_full[st], (f.idx >> 1) & 1,
-                                                  abort_flag, dev_status)) {
+                    umma_commit(&bars->m2_done[h]);
+                };
+                auto finish_later = [&]() {
+                    if (!later.on) return;
+                    later.on = false;
+                    second_products(1, later.st, later.cols, later.first);
+                    if (!ok) return;
+                    umma_commit(&bars->y_empty[later.st]);
+                    if (later.last) umma_commit(&bars->acc_full);
+                };
+                uint32_t fill = 0;  // every step has its own fill
+                for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
+                    if (!wk.has()) continue;
+                    const BandItem it = decode_band(wk.cur);
+                    const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, 0, G, p);
+                    for (int s = 0; ok && s < o.n_sub; ++s, ++fill) {
+                        const uint32_t st = fill & 1;
+                        // a step over the sinks alone takes their columns only (whole K = 16 slices)
+                        const uint32_t all = !KEYMAJOR && o.sink0 && s == 0 ? (p.sinks + 15) & ~15 : kBlockN;
+                        const uint32_t c0 = all < kHalf ? all : kHalf, c1 = all - c0;
+                        if (s == 0) {
+                            finish_later();  // before the wait for X: the last tile's epilogue waits for it
+                            ok = ok && mbar_wait(&bars->x_full, oc & 1, abort_flag, dev_status);
+                        }
+                        ok = ok && mbar_wait(&bars->y_ok[st], (fill >> 1) & 1, abort_flag, dev_status);
+                        if (ok) first_products(0, st, c0);
+                        if (ok) finish_later();
+                        if (ok) first_products(1, st, c1);
+                        if (!ok) break;
+                        if (s + 1 == o.n_sub) umma_commit(&bars->x_empty);
+                        if (s == 0 && oc > 0) ok = mbar_wait(&bars->acc_empty, (oc - 1) & 1, abort_flag, dev_status);
+                        if (ok) second_products(0, st, c0, s == 0);
+                        later = {true, s == 0, s + 1 == o.n_sub, st, c1};
+                    }
+                    ++oc;
+                }
+                if (ok) finish_later();
+            } else {
+                for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
+                    if (!wk.has()) continue;
+                    const BandItem it = decode_band(wk.cur);
+                    if (!item_used<KEYMAJOR>(it, G)) continue;
+                    for (int u = 0; ok && u < it.n_qt; ++u) {
+                        const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, u, G, p);
+                        if (!mbar_wait(&bars->x_full, oc & 1, abort_flag, dev_status)) {
                             ok = false;
                             break;
                         }
-                        // S = X0 Y0^T and dP = X1 Y1^T at full width (N = 128); their columns are free
-                        // once the previous step's second products of both halves are done
-                        for (int h = 0; ok && h < 2; ++h)
-                            if (sc > 0 && !mbar_wait(&bars->m2_done[h], (sc - 1) & 1, abort_flag,
-                                                     dev_status))
-                                ok = false;
-                        if (!ok) break;
-                        tc_fence_after();
-                        // a step over the sinks alone takes the first sink_cols columns only
-                        const bool sink_step = SINK && !KEYMAJOR && o.sink0 && s == 0;
-                        const uint32_t id1 = sink_step ? idesc_sink : idesc1;
-#pragma unroll
-                        for (int kk = 0; kk < HD / 16; ++kk) {
-                            umma_f16_ss(tm_s, desc_kmajor(x0, kk), desc_kmajor(y0, kk), id1,
-                                        kk == 0 ? 0u : 1u);
-                            umma_f16_ss(tm_dp, desc_kmajor(x1, kk), desc_kmajor(y1, kk), id1,
-                                        kk == 0 ? 0u : 1u);
-                        }
-                        umma_commit(&bars->s_full[0]);  // one per elementwise warpgroup
-                        umma_commit(&bars->s_full[1]);
-                        if (!ok) break;
-                        if (s + 1 == o.n_sub) umma_commit(&bars->x_empty);
-                        // second products of half h: K = the half's 64 Y rows
-                        for (int h = 0; ok && h < 2; ++h) {
-                            if (!mbar_wait(&bars->p_full[h], sc & 1, abort_flag, dev_status) ||
-                                (s == 0 && h == 0 && oc > 0 &&
-                                 !mbar_wait(&bars->acc_empty, (oc - 1) & 1, abort_flag, dev_status))) {
+                        for (int s = 0; s < o.n_sub; ++s) {
+                            const StepFill f = ft.step(reuse, u, it.n_qt, s, o.n_sub);
+                            const uint32_t st = f.idx & 1;
+                            const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile, y1 = y0 + L::kTile;
+                            // each fill is waited for once, by its first reader, in fill order
+                            if (f.first &&
+                                !mbar_wait(&bars->y_full[st], (f.idx >> 1) & 1, abort_flag, dev_status)) {
                                 ok = false;
                                 break;
                             }
+                            // S = X0 Y0^T and dP = X1 Y1^T at full width (N = 128); their columns are free
+                            // once the previous step's second products of both halves are done
+                            for (int h = 0; ok && h < 2; ++h)
+                                if (sc > 0 && !mbar_wait(&bars->m2_done[h], (sc - 1) & 1, abort_flag,
+                                                         dev_status))
+                                    ok = false;
+                            if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const uint32_t acc = (s > 0 || h > 0 || kk > 0) ? 1u : 0u;
-                                if (SINK && !KEYMAJOR && sink_step && 64 * h + 16 * kk >= sink_cols) continue;
-                                umma_f16_ts(tm_acc_ds, tm_dp + 64 * h + 8 * kk, desc_v(y0, 4 * h + kk),
-                                            idesc2, acc);
-                                if (KEYMAJOR)
-                                    umma_f16_ts(tm_acc_p, tm_s + 64 * h + 8 * kk, desc_v(y1, 4 * h + kk),
-                                                idesc2, acc);
+                            for (int kk = 0; kk < HD / 16; ++kk) {
+                                umma_f16_ss(tm_s, desc_kmajor(x0, kk), desc_kmajor(y0, kk), idesc1,
+                                            kk == 0 ? 0u : 1u);
+                                umma_f16_ss(tm_dp, desc_kmajor(x1, kk), desc_kmajor(y1, kk), idesc1,
+                                            kk == 0 ? 0u : 1u);
                             }
-                            umma_commit(&bars->m2_done[h]);
+                            umma_commit(&bars->s_full[0]);  // one per elementwise warpgroup
+                            umma_commit(&bars->s_full[1]);
+                            if (!ok) break;
+                            if (s + 1 == o.n_sub) umma_commit(&bars->x_empty);
+                            // second products of half h: K = the half's 64 Y rows
+                            for (int h = 0; ok && h < 2; ++h) {
+                                if (!mbar_wait(&bars->p_full[h], sc & 1, abort_flag, dev_status) ||
+                                    (s == 0 && h == 0 && oc > 0 &&
+                                     !mbar_wait(&bars->acc_empty, (oc - 1) & 1, abort_flag, dev_status))) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    const uint32_t acc = (s > 0 || h > 0 || kk > 0) ? 1u : 0u;
+                                    umma_f16_ts(tm_acc_ds, tm_dp + 64 * h + 8 * kk, desc_v(y0, 4 * h + kk),
+                                                idesc2, acc);
+                                    if (KEYMAJOR)
+                                        umma_f16_ts(tm_acc_p, tm_s + 64 * h + 8 * kk, desc_v(y1, 4 * h + kk),
+                                                    idesc2, acc);
+                                }
+                                umma_commit(&bars->m2_done[h]);
+                            }
+                            if (!ok) break;
+                            if (f.last) umma_commit(&bars->y_empty[st]);
+                            if (s + 1 == o.n_sub) umma_commit(&bars->acc_full);
+                            ++sc;
                         }
-                        if (!ok) break;
-                        if (f.last) umma_commit(&bars->y_empty[st]);
-                        if (s + 1 == o.n_sub) umma_commit(&bars->acc_full);
-                        ++sc;
+                        ++oc;
                     }
-                    ++oc;
                 }
             }
             // Wait (bounded) until every MMA this thread issued has finished.
@@ -559,8 +636,6 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->y_full[st], (f.idx >> 1) & 1,
                                                                abort_flag, dev_status));
                     if (!ok) break;
-                    const int w_lo = __reduce_min_sync(0xffffffffu, c_lo);
-                    const int w_hi = __reduce_max_sync(0xffffffffu, c_hi);
                     const float* l2v = vec + st * 256;
                     {
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[h], sc & 1, abort_flag,
@@ -611,9 +686,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                                     const int col = 32 * c + e + x;
                                     const float pe = ex2(fmaf(__uint_as_float(sv[32 * cc + e + x]), scale_log2, -l2q[x]));
                                     if (SINK) {
-                                        // a hidden weight becomes 0 by its bit's sign mask
-                                        pr[x] = __uint_as_float(__float_as_uint(pe) &
-                                                                static_cast<uint32_t>(static_cast<int32_t>(bits << (31 - (e + x))) >> 31));
+                                        pr[x] = ((bits >> (e + x)) & 1u) ? pe : 0.f;
                                     } else {
                                         const bool vis = col >= c_lo && col <= c_hi;
                                         pr[x] = vis ? pe : 0.f;
