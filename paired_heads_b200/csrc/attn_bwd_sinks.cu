@@ -1,0 +1,780 @@
+// attn_bwd_sinks.cu -- backward of causal attention with a sliding window and sinks on the sm_100a
+// tensor cores (bf16, head_dim 64 / 128), over tile lists.
+//
+// Mathematics: with P recomputed from q, k and the forward's lse, and D_i = dO_i . O_i,
+//   dP = dO V^T,  dS = P o (dP - D),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
+// Tiles of 128 slots are counted from the document's start. Query tile j sees the key tiles of its
+// window and, through the sinks (at most 128: they lie in key tile 0), key tile 0. One kernel template:
+//   key-major (dK, dV): outer tile X = (K, V) of a key tile, steps Y = (Q, dO) of the query tiles that
+//     see it, for every query head of the group: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO,
+//     dK += dS^T Q;
+//   query-major (dQ): X = (Q, dO) of a query tile, steps Y = (K, V) of the key tiles it sees:
+//     S = Q K^T, dP = dO V^T, dQ += dS K. Key tile 0 behind the window is a first step of as many
+//     columns as there are sinks (whole K = 16 slices).
+// Key tile 0 over the query tiles that only its sinks reach ("far") comes in pieces (kernels.cuh): their
+// float32 rows, like the window's part of the same rows, go to p.sink_part and are summed in order by
+// attn_bwd_sink_sum_kernel; so no CTA walks a whole document, and no atomics are used.
+//
+// What bounds it: the S and dP products read both operands from shared memory (128 bytes a clock: 64
+// clocks for each K = 16 slice of a 128 x 128 product, twice its tensor time), the others one; with 16
+// + 16 slices that is about 1,500 clocks a step (key-major), to which the chain S -> P -> dV -> S of
+// one step must not add up. So the elementwise work is cut in two, P from S (stage A) and dS from dP
+// (stage B), and each overlaps the other's products: while stage B runs, dV += P^T dO and the next S
+// are computed; while the next stage A runs, dK += dS^T Q and the next dP. (Both stages after both
+// products, as in attn_bwd_tc.cu: 798 us for dK / dV of 2 x 8192 tokens, 32 / 8 heads of 128, window
+// 1024, 675 for dQ; the two column halves of a step staggered instead: 680 and 574, the halves' N = 64
+// products reading X twice.)
+// TMEM columns: S [0, 128), dP [128, 256), accumulators from 256 (dV, dK or dQ). Key-major, P^T and dS^T
+// of column half h (bf16 A operands) overwrite the first 32 of the half's own S or dP columns;
+// query-major, dS goes to two buffers of 64 columns at 384 so that S and dP of the next step wait only
+// for their columns to have been read.
+//
+// CTA = 12 warps, one per SM, persistent over the list (items dealt in snake order):
+//   warps 0-7   two warpgroups, warpgroup h taking columns 64 h .. 64 h + 63 of every step (row = TMEM
+//               lane) and half h of the accumulator columns in the epilogue
+//   warp 8      producer (TMA; key-major also lse log2(e) and D of the fill's queries)
+//   warp 9      MMA issuer, owner of the 512 TMEM columns
+//   warps 10-11 blank the rows of each landed Y tile that lie behind the document's end: whatever is there
+//               (a padded batch's NaN) would meet a zero weight, and 0 * NaN is NaN
+// Every wait is bounded (1 s); on expiry the CTA records a status, drains its own copies and MMAs,
+// frees TMEM and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_common.cuh"
+#include "kernels.cuh"
+
+namespace pha {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsElementwise = 200, kRegsOther = 104;
+static_assert(8 * kRegsElementwise + 4 * kRegsOther <= 12 * 168, "register split");
+
+template <int HD, bool KEYMAJOR>
+struct Layout {
+    static constexpr int kChunk = 128 * 128;  // one [128 rows][64 bf16] swizzled chunk (bytes)
+    static constexpr int kTile = 128 * HD * 2;
+    static constexpr int kOffX = 0;                        // X0, X1
+    static constexpr int kOffY = kOffX + 2 * kTile;        // [2 stages] Y0, Y1
+    // key-major: [2 stages] lse2[128], D[128]; then 2 KB per warp (a 16-row box of dK / dV on its way
+    // out); query-major: the dQ tile on its way out
+    static constexpr int kOffVec = kOffY + 4 * kTile;
+    static constexpr int kOffStg = kOffVec + (KEYMAJOR ? 2 * 2 * 128 * 4 : 0);
+    static constexpr int kOffBar = kOffStg + (KEYMAJOR ? 8 * 2048 : kTile);
+    static constexpr int kBarBytes = 256;
+    static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + slack to align to 1024
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kTmS = 0, kTmDP = 128, kTmAcc = 256, kTmDS = 384;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct Bars {
+    uint64_t x_full, x_empty;
+    uint64_t y_full[2], y_ok[2], y_empty[2];
+    uint64_t s_full, dp_full;   // a step's S / dP are in TMEM
+    uint64_t a_done, b_done;    // stage A / B done by both warpgroups (key-major: P / dS stored; query-major,
+                                // a_done: S read, b_done: dS stored)
+    uint64_t dp_read;           // query-major: dP read
+    uint64_t m2a_done;          // key-major: dV product complete (P's columns are free)
+    uint64_t m2b_done[2];       // dK product complete (key-major: [0]) or dQ's of dS buffer i
+    uint64_t acc_full, acc_empty, drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// The low n bits (n clamped to 0 .. 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// An item of the list: its outer tile and the steps over it.
+struct Tile {
+    int row0;            // first slot of the outer tile
+    int head;            // query head (query-major) or kv head (key-major)
+    int doc_start, doc_end;
+    int n_sub;           // steps
+    int nq;              // key-major: query tiles per head
+    int first;           // document tile of the first step's Y tile
+    bool sink0;          // query-major: step 0 is key tile 0, the others follow from `first`
+    int piece;           // key-major: far piece, or -1
+};
+
+template <bool KEYMAJOR>
+__device__ __forceinline__ Tile decode_tile(int4 w, const AttnProblem& p, int G) {
+    const BandItem it = decode_band(w);
+    Tile o;
+    o.row0 = it.q0;
+    o.doc_start = it.doc_start;
+    o.doc_end = it.doc_end;
+    o.sink0 = false;
+    o.piece = -1;
+    const int a = it.doc_start, b = it.doc_end;
+    const int j = (o.row0 - a) / kBlockN, last = (b - a - 1) / kBlockN;
+    int lo, hi;
+    if (!KEYMAJOR) {
+        o.head = it.head;
+        lo = p.window > 0 && o.row0 - p.window + 1 > a ? (o.row0 - p.window + 1 - a) / kBlockN : 0;
+        hi = j;
+        o.nq = 0;
+        o.sink0 = p.sinks > 0 && lo > 0;
+        o.n_sub = hi - lo + 1 + (o.sink0 ? 1 : 0);
+    } else {
+        o.head = it.head / G;
+        if (it.n_qt > 1) {
+            o.piece = it.n_qt - 2;
+            const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
+            lo = sink_far_tile(p.window, b - a) + o.piece * c;
+            hi = min(last, lo + c - 1);
+        } else {
+            lo = j;
+            hi = last;
+            if (p.window > 0) {
+                const int n_rows = min(kBlockM, b - o.row0);
+                const int q_last = o.row0 + n_rows - 1 + p.window - 1;
+                hi = (min(q_last, b - 1) - a) / kBlockN;
+            }
+        }
+        o.nq = hi - lo + 1;
+        o.n_sub = G * o.nq;
+    }
+    o.first = lo;
+    return o;
+}
+
+// Step s: the head and first slot of its Y tiles.
+template <bool KEYMAJOR>
+__device__ __forceinline__ void step_tile(const Tile& o, int s, int G, int& y_head, int& y_row) {
+    if (KEYMAJOR) {
+        y_head = o.head * G + s / o.nq;
+        y_row = o.doc_start + kBlockN * (o.first + s % o.nq);
+    } else {
+        y_head = o.head / G;
+        y_row = o.doc_start + kBlockN * (o.sink0 ? (s == 0 ? 0 : o.first + s - 1) : o.first + s);
+    }
+}
+
+// Columns of step s that are multiplied.
+template <bool KEYMAJOR>
+__device__ __forceinline__ int step_cols(const Tile& o, int s, const AttnProblem& p) {
+    return !KEYMAJOR && o.sink0 && s == 0 ? (p.sinks + 15) & ~15 : kBlockN;
+}
+
+template <int HD, bool KEYMAJOR>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_bwd_sinks_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                          const __grid_constant__ CUtensorMap tm_st, const __grid_constant__ CUtensorMap tm_st2,
+                          const AttnProblem p, const float* __restrict__ dsum, __nv_bfloat16* __restrict__ out_a,
+                          __nv_bfloat16* __restrict__ out_b, const int4* __restrict__ items, WorkspaceHeader* hdr) {
+    // out_a: dQ (query-major) or dK (key-major); out_b: dV (key-major); tm_st: a map over dQ with a 64 x
+    // 32 box or over dK with a 64 x 16 box; tm_st2: over dV with a 64 x 16 box (key-major)
+    using L = Layout<HD, KEYMAJOR>;
+    static_assert(sizeof(Bars) <= L::kBarBytes, "barrier block");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
+    const uint32_t sbase = smem_u32(smem);
+    Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
+    float* vec = reinterpret_cast<float*>(smem + L::kOffVec);
+    volatile int* abort_flag = &bars->abort;
+    int* dev_status = &hdr->status;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (warp == 8 && lane == 0) {
+        mbar_init(&bars->x_full, 1);
+        mbar_init(&bars->x_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            // the TMA arrival, plus (key-major) the 32 producer lanes after writing lse2 / D
+            mbar_init(&bars->y_full[s], KEYMAJOR ? 33 : 1);
+            mbar_init(&bars->y_ok[s], 64);
+            mbar_init(&bars->y_empty[s], 1);
+            mbar_init(&bars->m2b_done[s], 1);
+        }
+        mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->dp_full, 1);
+        mbar_init(&bars->a_done, 256);
+        mbar_init(&bars->b_done, 256);
+        mbar_init(&bars->dp_read, 256);
+        mbar_init(&bars->m2a_done, 1);
+        mbar_init(&bars->acc_full, 1);
+        mbar_init(&bars->acc_empty, 256);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_do);
+    }
+    if (warp == 9) {
+        tmem_alloc(&bars->tmem_base, L::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    const int n_items = *reinterpret_cast<volatile int*>(&hdr->n_items);
+    const int H = p.heads, Hkv = p.kv_heads, G = H / Hkv;
+    // key-major: one item per kv head (that of the group's first query head)
+    const int walk_g = KEYMAJOR ? G : 1;
+    if (warp >= 8) regs_decrease<kRegsOther>();
+
+    if (warp >= 10) {
+        // ------------------------------------------------------------ blank rows behind the document
+        const int at = threadIdx.x - 320;  // 0 .. 63
+        uint32_t n = 0;                    // fills so far (every step has its own)
+        bool ok = true;
+        ItemWalk wk;
+        for (wk.start(items, n_items, walk_g, H); ok && !wk.done(); wk.advance()) {
+            if (!wk.has()) continue;
+            const Tile o = decode_tile<KEYMAJOR>(wk.cur, p, G);
+            for (int s = 0; s < o.n_sub; ++s, ++n) {
+                const uint32_t st = n & 1;
+                ok = mbar_wait(&bars->y_full[st], (n >> 1) & 1, abort_flag, dev_status);
+                if (!ok) break;
+                int y_head, y_row;
+                step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
+                const int rows = o.doc_end - y_row;  // rows of the document
+                if (rows < kBlockN) {
+                    uint8_t* y = smem + L::kOffY + st * 2 * L::kTile;
+                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                    // a row is 128 bytes of each 64-column chunk (the swizzle stays inside them)
+                    for (int x = at; x < (kBlockN - rows) * 8; x += 64)
+#pragma unroll
+                        for (int c = 0; c < 2 * HD / 64; ++c)
+                            *reinterpret_cast<uint4*>(y + c * L::kChunk + rows * 128 + x * 16) = z;
+                    fence_proxy_async_smem();
+                }
+                mbar_arrive(&bars->y_ok[st]);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ producer
+        // X = (K, V) and Y = (Q, dO) (key-major), or the other way round
+        const CUtensorMap* mx0 = KEYMAJOR ? &tm_k : &tm_q;
+        const CUtensorMap* mx1 = KEYMAJOR ? &tm_v : &tm_do;
+        const CUtensorMap* my0 = KEYMAJOR ? &tm_q : &tm_k;
+        const CUtensorMap* my1 = KEYMAJOR ? &tm_do : &tm_v;
+        uint32_t oc = 0, n = 0;  // outer tiles and fills issued so far
+        bool ok = true;
+        auto acquire = [&](uint64_t* bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
+        };
+        auto load_y = [&](const Tile& o, int s) -> bool {
+            const uint32_t st = n & 1;
+            if (!acquire(&bars->y_empty[st], ((n >> 1) & 1) ^ 1)) return false;
+            ++n;
+            int y_head, y_row;
+            step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->y_full[st], 2 * L::kTile);
+                uint8_t* y = smem + L::kOffY + st * 2 * L::kTile;
+                for (int c = 0; c < HD / 64; ++c) {
+                    tma_load_2d(y + c * L::kChunk, my0, y_head * HD + 64 * c, y_row, &bars->y_full[st]);
+                    tma_load_2d(y + L::kTile + c * L::kChunk, my1, y_head * HD + 64 * c, y_row, &bars->y_full[st]);
+                }
+            }
+            if (KEYMAJOR) {
+                // lse * log2(e) and D of the fill's queries (0 past the document end)
+                float* l2 = vec + st * 256;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 4 * lane + e, qs = y_row + c;
+                    const bool in = qs < o.doc_end;
+                    const int64_t r = static_cast<int64_t>(qs) * H + y_head;
+                    l2[c] = in ? p.lse[r] * kLog2e : 0.f;
+                    l2[128 + c] = in ? dsum[r] : 0.f;
+                }
+                mbar_arrive(&bars->y_full[st]);
+            }
+            return true;
+        };
+        ItemWalk wk;
+        for (wk.start(items, n_items, walk_g, H); ok && !wk.done(); wk.advance()) {
+            if (!wk.has()) continue;
+            const Tile o = decode_tile<KEYMAJOR>(wk.cur, p, G);
+            ok = load_y(o, 0);  // before X, whose buffer is free later
+            if (ok) ok = acquire(&bars->x_empty, (oc & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->x_full, 2 * L::kTile);
+                for (int c = 0; c < HD / 64; ++c) {
+                    tma_load_2d(smem + L::kOffX + c * L::kChunk, mx0, o.head * HD + 64 * c, o.row0, &bars->x_full);
+                    tma_load_2d(smem + L::kOffX + L::kTile + c * L::kChunk, mx1, o.head * HD + 64 * c, o.row0,
+                                &bars->x_full);
+                }
+            }
+            ++oc;
+            for (int s = 1; ok && s < o.n_sub; ++s) ok = load_y(o, s);
+        }
+        if (!ok && lane == 0) {
+            // Wait (bounded) for the copies this warp issued last into every buffer.
+            if (oc > 0) drain_wait(&bars->x_full, (oc - 1) & 1);
+            for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) drain_wait(&bars->y_full[i & 1], (i >> 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc1 = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
+            constexpr uint32_t idesc2 = idesc_bf16_f32(kBlockM, HD, 0, 1);
+            const uint32_t tm_s = tmem + L::kTmS, tm_dp = tmem + L::kTmDP;
+            const uint32_t x0 = sbase + L::kOffX, x1 = x0 + L::kTile;
+            uint32_t tiles = 0;   // outer tiles begun
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok) ok = mbar_wait(bar, parity, abort_flag, dev_status);
+            };
+            // The steps of all items in a row: where step g is, and the next one.
+            struct Step {
+                bool on, first, last;
+                int cols;
+            };
+            ItemWalk wk;
+            Tile o{};
+            int s = 0;
+            auto open = [&]() -> bool {  // the next item, if any
+                while (!wk.done() && !wk.has()) wk.advance();
+                if (wk.done()) return false;
+                o = decode_tile<KEYMAJOR>(wk.cur, p, G);
+                s = 0;
+                return true;
+            };
+            auto next = [&]() -> Step {
+                if (s == o.n_sub) {
+                    wk.advance();
+                    if (!open()) return Step{false, false, false, 0};
+                }
+                const Step x{true, s == 0, s + 1 == o.n_sub, step_cols<KEYMAJOR>(o, s, p)};
+                ++s;
+                return x;
+            };
+            // S or dP of step g: X (K-major) times Y (K-major), the first x.cols columns
+            auto product1 = [&](const Step& x, uint32_t g, uint32_t xt, int which, uint32_t d, uint64_t* full) {
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t id = (idesc1 & ~(0x3Fu << 17)) | (static_cast<uint32_t>(x.cols >> 3) << 17);
+                const uint64_t dx = desc_kmajor(xt, 0);
+                const uint64_t dy = desc_kmajor(sbase + L::kOffY + (g & 1) * 2 * L::kTile + which * L::kTile, 0);
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {  // (as desc_kmajor steps)
+                    const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                    umma_f16_ss(d, dx + step, dy + step, id, kk == 0 ? 0u : 1u);
+                }
+                umma_commit(full);
+            };
+            // acc += A (TMEM, bf16 pairs; column half h at a + h * half) times Y's rows (MN-major)
+            auto product2 = [&](const Step& x, uint32_t g, uint32_t a, uint32_t half, int which, uint32_t acc,
+                                uint64_t* done) {
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t dy = desc_v(sbase + L::kOffY + (g & 1) * 2 * L::kTile + which * L::kTile, 0);
+#pragma unroll
+                for (int kk = 0; kk < kBlockN / 16; ++kk) {
+                    if (!KEYMAJOR && 16 * kk >= x.cols) continue;
+                    umma_f16_ts(acc, a + (kk >> 2) * half + (kk & 3) * 8, dy + kk * (2048 >> 4), idesc2,
+                                (!x.first || kk > 0) ? 1u : 0u);
+                }
+                umma_commit(done);
+            };
+            // the tile and fill of a step about to be multiplied
+            auto wait_inputs = [&](const Step& x, uint32_t g) {
+                if (x.first) {
+                    wait(&bars->x_full, tiles & 1);
+                    ++tiles;
+                }
+                wait(&bars->y_ok[g & 1], (g >> 1) & 1);
+            };
+            wk.start(items, n_items, walk_g, H);
+            uint32_t g = 0;
+            Step cur = open() ? next() : Step{false, false, false, 0};
+            if (cur.on) {
+                wait_inputs(cur, 0);
+                product1(cur, 0, x0, 0, tm_s, &bars->s_full);
+                product1(cur, 0, x1, 1, tm_dp, &bars->dp_full);
+                if (ok && cur.last) umma_commit(&bars->x_empty);
+            }
+            for (; ok && cur.on; ++g) {
+                const Step nxt = next();
+                // a new outer tile's X comes when this one's last products are through: they go first
+                const bool early = nxt.on && !nxt.first;
+                // stage A's end: key-major dV += P^T dO, then (its P being S's columns) the next S; query-
+                // major the next S at once
+                wait(&bars->a_done, g & 1);
+                if (KEYMAJOR) {
+                    if (cur.first && tiles > 1) wait(&bars->acc_empty, tiles & 1);
+                    product2(cur, g, tm_s, 64, 1, tmem + L::kTmAcc, &bars->m2a_done);
+                }
+                if (early) {
+                    wait_inputs(nxt, g + 1);
+                    if (KEYMAJOR) wait(&bars->m2a_done, g & 1);
+                    product1(nxt, g + 1, x0, 0, tm_s, &bars->s_full);
+                    if (!KEYMAJOR) {
+                        wait(&bars->dp_read, g & 1);
+                        product1(nxt, g + 1, x1, 1, tm_dp, &bars->dp_full);
+                        if (ok && nxt.last) umma_commit(&bars->x_empty);
+                    }
+                }
+                // stage B's end: dK += dS^T Q, or dQ += dS K
+                wait(&bars->b_done, g & 1);
+                if (KEYMAJOR) {
+                    product2(cur, g, tm_dp, 64, 0, tmem + L::kTmAcc + HD, &bars->m2b_done[0]);
+                } else {
+                    if (cur.first && tiles > 1) wait(&bars->acc_empty, tiles & 1);
+                    product2(cur, g, tmem + L::kTmDS + 64 * (g & 1), 32, 0, tmem + L::kTmAcc, &bars->m2b_done[g & 1]);
+                }
+                if (!ok) break;
+                umma_commit(&bars->y_empty[g & 1]);
+                if (cur.last) umma_commit(&bars->acc_full);
+                if (nxt.on && !early) {
+                    wait_inputs(nxt, g + 1);
+                    if (KEYMAJOR) wait(&bars->m2a_done, g & 1);
+                    product1(nxt, g + 1, x0, 0, tm_s, &bars->s_full);
+                    if (!KEYMAJOR) {
+                        wait(&bars->dp_read, g & 1);
+                        product1(nxt, g + 1, x1, 1, tm_dp, &bars->dp_full);
+                        if (ok && nxt.last) umma_commit(&bars->x_empty);
+                    }
+                }
+                if (KEYMAJOR && nxt.on) {  // dS lay in dP's columns
+                    wait(&bars->m2b_done[0], g & 1);
+                    product1(nxt, g + 1, x1, 1, tm_dp, &bars->dp_full);
+                    if (ok && nxt.last) umma_commit(&bars->x_empty);
+                }
+                cur = nxt;
+            }
+            // Wait (bounded) until every MMA this thread issued has finished.
+            umma_commit(&bars->drain);
+            drain_wait(&bars->drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ elementwise warpgroups
+        regs_increase<kRegsElementwise>();
+        const int h = warp >> 2;            // the column half of every step this warpgroup takes
+        const int row = threadIdx.x & 127;  // TMEM lane == row of the outer tile
+        const int r0 = (warp & 3) * 32;     // first row of this warp
+        const uint32_t tm_lane = tmem + (static_cast<uint32_t>(r0) << 16);
+        const float scale_log2 = p.scale * kLog2e;
+        const int window = p.window;
+        uint32_t oc = 0, g = 0;  // outer tiles and steps done
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
+            return ok;
+        };
+        ItemWalk wk;
+        for (wk.start(items, n_items, walk_g, H); ok && !wk.done(); wk.advance()) {
+            if (!wk.has()) continue;
+            const Tile o = decode_tile<KEYMAJOR>(wk.cur, p, G);
+            const int a = o.doc_start, b = o.doc_end;
+            const int slot = o.row0 + row;  // key slot (key-major) or query slot
+            const bool valid = slot < b;
+            float lse2 = 0.f, dd = 0.f;     // query-major: this row's lse * log2(e) and D
+            if (!KEYMAJOR && valid) {
+                const int64_t r = static_cast<int64_t>(slot) * H + o.head;
+                lse2 = p.lse[r] * kLog2e;
+                dd = dsum[r];
+            }
+            for (int s = 0; s < o.n_sub; ++s, ++g) {
+                const uint32_t st = g & 1;
+                int y_head, y_row;
+                step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
+                // visible columns of this row: [c_lo, c_hi], and those below c_sk
+                int c_lo, c_hi, c_sk = 0;
+                if (KEYMAJOR) {  // the queries that see key `slot`
+                    c_lo = slot - y_row;
+                    c_hi = (window > 0 && slot - a >= p.sinks ? min(slot + window - 1, b - 1) : b - 1) - y_row;
+                } else {         // the keys query `slot` sees
+                    c_lo = (window > 0 ? max(a, slot - window + 1) : a) - y_row;
+                    c_hi = slot - y_row;
+                    c_sk = a + p.sinks - y_row;
+                }
+                if (!valid) c_hi = -1;
+                // What nobody reads is left out: columns behind the sinks' slices in a step over them alone,
+                // rows that are no sinks in a far piece (their sums are not kept).
+                const int n_cols = step_cols<KEYMAJOR>(o, s, p);
+                const bool idle = 64 * h >= n_cols || (KEYMAJOR && o.piece >= 0 && r0 >= p.sinks);
+                const float* l2v = vec + st * 256 + 64 * h;
+                // stage A: P of the half's 64 columns, kept for stage B in registers
+                float pr[64];
+                if (KEYMAJOR && !wait(&bars->y_full[st], (g >> 1) & 1)) break;  // lse2 / D
+                if (!wait(&bars->s_full, g & 1)) break;
+                tc_fence_after();
+                if (!idle) {
+                    uint32_t sv[64];
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) tmem_ld32(tm_lane + L::kTmS + 64 * h + 32 * cc, sv + 32 * cc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) regs_after_wait(sv + 32 * cc);
+                    if (!KEYMAJOR) {
+                        tc_fence_before();  // S may be overwritten from here on
+                        mbar_arrive(&bars->a_done);
+                    }
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        const int cb = 64 * h + 32 * cc;
+                        const uint32_t bits = low_bits(c_hi + 1 - cb) & (~low_bits(c_lo - cb) | low_bits(c_sk - cb));
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float4 l4 = make_float4(lse2, lse2, lse2, lse2);
+                            if (KEYMAJOR) l4 = *reinterpret_cast<const float4*>(l2v + 32 * cc + e);
+                            const float l2q[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float pe = ex2(fmaf(__uint_as_float(sv[32 * cc + e + x]), scale_log2, -l2q[x]));
+                                pr[32 * cc + e + x] = ((bits >> (e + x)) & 1u) ? pe : 0.f;
+                            }
+                        }
+                    }
+                    if (KEYMAJOR) {
+                        // P rounded to bf16 as the A operand of dV += P^T dO (stage B takes it unrounded)
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
+                        tmem_st32(tm_lane + L::kTmS + 64 * h, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&bars->a_done);
+                    }
+                } else {
+                    tc_fence_before();
+                    mbar_arrive(&bars->a_done);
+                }
+                // stage B: dS = P (dP - D)
+                if (!wait(&bars->dp_full, g & 1)) break;
+                tc_fence_after();
+                if (!idle) {
+                    uint32_t dv[64];
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) tmem_ld32(tm_lane + L::kTmDP + 64 * h + 32 * cc, dv + 32 * cc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) regs_after_wait(dv + 32 * cc);
+                    if (!KEYMAJOR) {
+                        tc_fence_before();  // dP may be overwritten from here on
+                        mbar_arrive(&bars->dp_read);
+                    }
+                    uint32_t dk[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        float4 d4 = make_float4(dd, dd, dd, dd);
+                        if (KEYMAJOR) d4 = *reinterpret_cast<const float4*>(l2v + 128 + e);
+                        dk[e >> 1] = pack_bf16x2(pr[e] * (__uint_as_float(dv[e]) - d4.x),
+                                                 pr[e + 1] * (__uint_as_float(dv[e + 1]) - d4.y));
+                        dk[(e >> 1) + 1] = pack_bf16x2(pr[e + 2] * (__uint_as_float(dv[e + 2]) - d4.z),
+                                                       pr[e + 3] * (__uint_as_float(dv[e + 3]) - d4.w));
+                    }
+                    // query-major: the buffer's last product (two steps ago) must be through
+                    if (!KEYMAJOR && g >= 2 && !wait(&bars->m2b_done[st], ((g >> 1) & 1) ^ 1)) break;
+                    tmem_st32(KEYMAJOR ? tm_lane + L::kTmDP + 64 * h : tm_lane + L::kTmDS + 64 * st + 32 * h, dk);
+                    tmem_wait_st();
+                } else if (!KEYMAJOR) {
+                    mbar_arrive(&bars->dp_read);
+                }
+                tc_fence_before();
+                mbar_arrive(&bars->b_done);
+            }
+            if (!ok) break;
+            // epilogue: accumulators -> bf16 rows of dQ, or of dK (scaled) and dV
+            if (!wait(&bars->acc_full, oc & 1)) break;
+            ++oc;
+            tc_fence_after();
+            const int out_heads = KEYMAJOR ? Hkv : H;
+            const int64_t base = (static_cast<int64_t>(slot) * out_heads + o.head) * HD;
+            bool store = true;  // rows of dQ, dK, dV in bf16
+            if (KEYMAJOR && p.sinks > 0 && window > 0 && o.row0 == a) {
+                // key tile 0: where the document has far query tiles, the sinks' rows of this part
+                const int64_t slots = b - a;
+                const int far = sink_far_tile(window, slots);
+                if (far * static_cast<int64_t>(kBlockN) < slots) {
+                    store = o.piece < 0;
+                    int d = -1, z = p.batch;  // the document: last one that starts at or before
+                    while (z - d > 1) {
+                        const int mid = (d + z) >> 1;
+                        if (static_cast<int64_t>(p.cu_seqlens[mid]) * p.slot_mult <= a) d = mid; else z = mid;
+                    }
+                    const int c = sink_piece_tiles(window, p.max_len, p.slot_mult);
+                    const int64_t q_first = a + static_cast<int64_t>(far + o.piece * c) * kBlockN;
+                    const int64_t part = o.piece < 0 ? d : p.batch + d + q_first / (static_cast<int64_t>(c) * kBlockN);
+                    float* dst = p.sink_part + ((part * Hkv + o.head) * p.sinks + row) * 2 * HD;
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w) {
+#pragma unroll 1
+                        for (int cc = h * (HD / 64); cc < (h + 1) * (HD / 64); ++cc) {
+                            uint32_t v[32];
+                            tmem_ld32(tm_lane + L::kTmAcc + (w == 0 ? HD : 0) + 32 * cc, v);
+                            tmem_wait_ld();
+                            regs_after_wait(v);
+                            const float mul = w == 0 ? p.scale : 1.f;
+                            if (row < p.sinks)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<float4*>(dst + w * HD + 32 * cc + e) =
+                                        make_float4(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
+                                                    __uint_as_float(v[e + 2]) * mul, __uint_as_float(v[e + 3]) * mul);
+                        }
+                    }
+                }
+            }
+            // A warp whose 32 rows all lie inside the document (hd 128: warpgroup h owns the 64-column chunk
+            // h) sends them out by TMA, dQ as one 32-row box, dK and dV 16 rows at a time through its 2 KB
+            // box; otherwise every thread stores its own row.
+            const bool boxes = store && HD == 128 && o.row0 + r0 + 31 < b;
+#pragma unroll 1
+            for (int w = 0; store && w < (KEYMAJOR ? 2 : 1); ++w) {
+                // w = 0: the dS product (dQ or dK, times scale); w = 1: dV
+                const uint32_t col0 = L::kTmAcc + (KEYMAJOR && w == 0 ? HD : 0);
+                const float mul = w == 0 ? p.scale : 1.f;
+                uint4 w8[HD / 16];  // this half's columns of the row
+#pragma unroll
+                for (int cc = 0; cc < HD / 64; ++cc) {
+                    uint32_t v[32];
+                    tmem_ld32(tm_lane + col0 + 32 * (h * (HD / 64) + cc), v);
+                    tmem_wait_ld();
+                    regs_after_wait(v);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4)
+                        w8[4 * cc + q4] = make_uint4(
+                            pack_bf16x2(__uint_as_float(v[8 * q4 + 0]) * mul, __uint_as_float(v[8 * q4 + 1]) * mul),
+                            pack_bf16x2(__uint_as_float(v[8 * q4 + 2]) * mul, __uint_as_float(v[8 * q4 + 3]) * mul),
+                            pack_bf16x2(__uint_as_float(v[8 * q4 + 4]) * mul, __uint_as_float(v[8 * q4 + 5]) * mul),
+                            pack_bf16x2(__uint_as_float(v[8 * q4 + 6]) * mul, __uint_as_float(v[8 * q4 + 7]) * mul));
+                }
+                if (!boxes) {
+                    __nv_bfloat16* dst = (w == 0 ? out_a : out_b) + base + h * (HD / 2);
+                    if (valid)
+#pragma unroll
+                        for (int u = 0; u < HD / 16; ++u) *reinterpret_cast<uint4*>(dst + 8 * u) = w8[u];
+                } else if (KEYMAJOR) {
+                    uint8_t* stg = smem + L::kOffStg + warp * 2048;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        if ((lane >> 4) == half) {
+                            const int r = lane & 15;  // row of the 16-row box
+#pragma unroll
+                            for (int u = 0; u < HD / 16; ++u)
+                                *reinterpret_cast<uint4*>(stg + r * 128 + ((u ^ (r & 7)) << 4)) = w8[u];
+                        }
+                        fence_proxy_async_smem();  // the rows are read by the async proxy (TMA)
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(w == 0 ? &tm_st : &tm_st2, o.head * HD + 64 * h, o.row0 + r0 + 16 * half, stg);
+                            tma_store_commit();
+                            tma_store_wait_read();  // the box is rewritten next
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    uint8_t* stg = smem + L::kOffStg + h * L::kChunk;
+#pragma unroll
+                    for (int u = 0; u < HD / 16; ++u)
+                        *reinterpret_cast<uint4*>(stg + row * 128 + ((u ^ (row & 7)) << 4)) = w8[u];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tm_st, o.head * HD + 64 * h, o.row0 + r0, stg + r0 * 128);
+                        tma_store_commit();
+                        tma_store_wait_read();  // the staging area is rewritten by the next tile
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars->acc_empty);
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    if (warp < 8 && lane == 0) tma_store_wait_all();  // the epilogue's TMA stores have completed
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, L::kTmemCols);
+}
+
+// Block (document, kv head, 256 of the values): the sinks' rows of dk, dv of documents with far query
+// tiles, summed over the window's part and the pieces in order.
+__global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProblem p, __nv_bfloat16* dk,
+                                                                __nv_bfloat16* dv, const WorkspaceHeader* hdr) {
+    if (hdr->status != DEV_OK) return;
+    const int d = blockIdx.x, g = blockIdx.y, hd = p.head_dim;
+    const int64_t a = static_cast<int64_t>(p.cu_seqlens[d]) * p.slot_mult;
+    const int64_t slots = static_cast<int64_t>(p.cu_seqlens[d + 1]) * p.slot_mult - a;
+    if (slots == 0) return;
+    const int far = sink_far_tile(p.window, slots);
+    const int n_far = static_cast<int>((slots + kBlockN - 1) / kBlockN) - far;
+    if (n_far <= 0) return;
+    const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
+    const int pieces = (n_far + c - 1) / c;
+    // pieces start exactly one piece apart: consecutive places
+    const int64_t place = p.batch + d + (a + static_cast<int64_t>(far) * kBlockN) / (static_cast<int64_t>(c) * kBlockN);
+    const int width = p.sinks * 2 * hd;
+    const int x = blockIdx.z * 256 + threadIdx.x;
+    if (x >= width) return;
+    const int64_t stride = static_cast<int64_t>(p.kv_heads) * width;
+    const float* rest = p.sink_part + (place * p.kv_heads + g) * width + x;
+    float sum = p.sink_part[(static_cast<int64_t>(d) * p.kv_heads + g) * width + x];
+#pragma unroll 8
+    for (int f = 0; f < pieces; ++f) sum += rest[f * stride];
+    const int m = x / (2 * hd), e = x % (2 * hd);  // (a document with far tiles has more than `sinks` rows)
+    const int64_t row = ((a + m) * p.kv_heads + g) * hd;
+    if (e < hd) dk[row + e] = __float2bfloat16_rn(sum);
+    else dv[row + e - hd] = __float2bfloat16_rn(sum);
+}
+
+template <int HD, bool KEYMAJOR>
+cudaError_t launch_one(const AttnProblem& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const CUtensorMap& tdo, const CUtensorMap& tst, const CUtensorMap& tst2, const float* dsum,
+                       void* out_a, void* out_b, const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
+    using L = Layout<HD, KEYMAJOR>;
+    int dev = 0, sms = 0;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(attn_bwd_sinks_kernel<HD, KEYMAJOR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  L::kSmemBytes)) != cudaSuccess ||
+        (e = cudaGetDevice(&dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
+    attn_bwd_sinks_kernel<HD, KEYMAJOR><<<sms, kThreads, L::kSmemBytes, stream>>>(
+        tq, tk, tv, tdo, tst, tst2, p, dsum, static_cast<__nv_bfloat16*>(out_a), static_cast<__nv_bfloat16*>(out_b),
+        items, hdr);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                     const CUtensorMap& tm_v, const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
+                                     const float* dsum, void* dq, const int4* items, WorkspaceHeader* hdr,
+                                     cudaStream_t stream) {
+    if (p.head_dim == 128)
+        return launch_one<128, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, dsum, dq, nullptr, items, hdr, stream);
+    if (p.head_dim == 64)
+        return launch_one<64, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, dsum, dq, nullptr, items, hdr, stream);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                       const CUtensorMap& tm_v, const CUtensorMap& tm_do, const CUtensorMap& tm_dk,
+                                       const CUtensorMap& tm_dv, const float* dsum, void* dk, void* dv,
+                                       const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
+    cudaError_t e = cudaErrorInvalidValue;
+    if (p.head_dim == 128)
+        e = launch_one<128, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, dsum, dk, dv, items, hdr, stream);
+    else if (p.head_dim == 64)
+        e = launch_one<64, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, dsum, dk, dv, items, hdr, stream);
+    if (e != cudaSuccess || p.sinks == 0) return e;
+    attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads, (p.sinks * 2 * p.head_dim + 255) / 256), 256, 0, stream>>>(
+        p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr);
+    return cudaGetLastError();
+}
+
+}  // namespace pha

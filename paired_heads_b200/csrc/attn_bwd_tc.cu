@@ -33,12 +33,6 @@
 //   warp 8     producer: X tiles (one buffer), Y tiles (two-slot ring) by TMA; in the key-major
 //              instance also lse * log2(e) and D of the fill's 128 queries into shared memory
 //   warp 9     MMA issuer, owner of the 512 TMEM columns
-// SINK (tile lists, causal): query tiles also see the first `sinks` slots of the document, which lie
-// in its key tile 0. dQ takes that tile as an extra first step. dK / dV of tile 0 over the query tiles
-// that only its sinks reach come in pieces (kernels.cuh), whose float32 rows, like the window's part of
-// the same rows, go to p.sink_part and are summed in order by attn_bwd_sink_sum_kernel. Warps 10 and
-// 11 blank the rows of each landed Y tile that lie behind the document's end: whatever is there (a
-// padded batch's NaN) would meet a zero weight, and 0 * NaN is NaN.
 // Every wait is bounded (1 s); on expiry the CTA records a status, drains its own copies and
 // MMAs, frees TMEM and exits.
 #include <cuda.h>
@@ -86,11 +80,7 @@ struct BwdBars {
     uint64_t acc_full, acc_empty, drain;
     uint32_t tmem_base;
     int abort;
-    uint64_t y_ok[2];  // SINK: the landed Y tiles' rows behind the document are blank
 };
-
-// The low n bits (n clamped to 0 .. 32).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
 // The steps of one outer tile (u-th tile of a band item, or the tile of a tile item).
 struct OuterTile {
@@ -98,21 +88,17 @@ struct OuterTile {
     int n_sub;    // inner steps
     int nq;       // key-major: query tiles per head (band: 1 or 2)
     int first;    // GEN: document tile index of the first inner step's Y tile
-    bool sink0;   // SINK, query-major: step 0 is key tile 0, the others follow from `first`
-    int piece;    // SINK, key-major: far piece, or -1
 };
 
 // GEN (tile items, any causal / window setting): query-major, the key tiles the query tile sees;
 // key-major, the query tiles that see the key tile, for every query head of its group. Tiles are
 // the document's 128-slot tiles counted from its start.
-template <bool KEYMAJOR, bool GEN, bool SINK>
+template <bool KEYMAJOR, bool GEN>
 __device__ __forceinline__ OuterTile outer_tile(const BandItem& it, int u, int G,
                                                 const AttnProblem& p) {
     OuterTile o;
     o.row0 = it.q0 + kBlockM * u;
     o.first = 0;
-    o.sink0 = false;
-    o.piece = -1;
     if (GEN) {
         const int a = it.doc_start, b = it.doc_end;
         const int j = (o.row0 - a) / kBlockN, last = (b - a - 1) / kBlockN;
@@ -123,15 +109,7 @@ __device__ __forceinline__ OuterTile outer_tile(const BandItem& it, int u, int G
                 if (p.window > 0 && o.row0 - p.window + 1 > a) lo = (o.row0 - p.window + 1 - a) / kBlockN;
             }
             o.nq = 0;
-            o.sink0 = SINK && p.sinks > 0 && lo > 0;
-            o.n_sub = hi - lo + 1 + (o.sink0 ? 1 : 0);
-        } else if (SINK && it.n_qt > 1) {
-            o.piece = it.n_qt - 2;
-            const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
-            lo = sink_far_tile(p.window, b - a) + o.piece * c;
-            hi = min(last, lo + c - 1);
-            o.nq = hi - lo + 1;
-            o.n_sub = G * o.nq;
+            o.n_sub = hi - lo + 1;
         } else {
             if (p.causal) {
                 lo = j;
@@ -158,7 +136,7 @@ __device__ __forceinline__ OuterTile outer_tile(const BandItem& it, int u, int G
 }
 
 // Inner step s of an outer tile: the head and first slot of its Y tiles.
-template <bool KEYMAJOR, bool GEN, bool SINK>
+template <bool KEYMAJOR, bool GEN>
 __device__ __forceinline__ void inner_step(const BandItem& it, const OuterTile& o, int s, int G,
                                            int& y_head, int& y_row) {
     if (GEN) {
@@ -167,7 +145,7 @@ __device__ __forceinline__ void inner_step(const BandItem& it, const OuterTile& 
             y_row = it.doc_start + kBlockN * (o.first + s % o.nq);
         } else {
             y_head = it.head / G;
-            y_row = it.doc_start + kBlockN * (SINK && o.sink0 ? (s == 0 ? 0 : o.first + s - 1) : o.first + s);
+            y_row = it.doc_start + kBlockN * (o.first + s);
         }
         return;
     }
@@ -227,7 +205,7 @@ struct FillTrack {
     }
 };
 
-template <int HD, bool KEYMAJOR, bool GEN, bool SINK>
+template <int HD, bool KEYMAJOR, bool GEN>
 __global__ void __launch_bounds__(kBwdTcThreads, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
@@ -243,7 +221,6 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
     // 64 x 16 box (key-major)
     using L = BwdLayout<HD, KEYMAJOR>;
     static_assert(sizeof(BwdBars) <= L::kBarBytes, "barrier block");
-    static_assert(!SINK || GEN, "the sinks come over tile lists");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
@@ -263,7 +240,6 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
             // the TMA arrival, plus (key-major) the 32 producer lanes after writing lse2 / D
             mbar_init(&bars->y_full[s], KEYMAJOR ? 33 : 1);
             mbar_init(&bars->y_empty[s], 1);
-            mbar_init(&bars->y_ok[s], 64);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&bars->s_full[h], 1);
@@ -291,9 +267,8 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
 
     const int n_items = *reinterpret_cast<volatile int*>(&hdr->n_items);
     const int H = p.heads, Hkv = p.kv_heads, G = H / Hkv;
-    constexpr int kRegsOther = SINK ? 104 : kTcRegsOther;  // (the staggered issue holds more)
-    static_assert(8 * kTcRegsSoftmax + 4 * kRegsOther <= 12 * 168, "register split");
-    if (warp >= 8) regs_decrease<kRegsOther>();  // the whole third warpgroup, then its roles
+    static_assert(8 * kTcRegsSoftmax + 4 * kTcRegsOther <= 12 * 168, "register split");
+    if (warp >= 8) regs_decrease<kTcRegsOther>();  // the whole third warpgroup, then its roles
     const bool reuse = !GEN && (!KEYMAJOR || G == 1);
     // X = (K, V) and Y = (Q, dO) (key-major), or the other way round
     const CUtensorMap* mx0 = KEYMAJOR ? &tm_k : &tm_q;
@@ -302,37 +277,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
     const CUtensorMap* my1 = KEYMAJOR ? &tm_do : &tm_v;
 
     if (warp >= 10) {
-        // -------------------------------------------- SINK: blank rows; else idle (register split only)
-        if (SINK) {
-            const int at = threadIdx.x - 320;  // 0 .. 63
-            uint32_t n = 0;                    // fills so far (every step has its own)
-            bool ok = true;
-            ItemWalk wk;
-            for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
-                if (!wk.has()) continue;
-                const BandItem it = decode_band(wk.cur);
-                const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, 0, G, p);
-                for (int s = 0; s < o.n_sub; ++s, ++n) {
-                    const uint32_t st = n & 1;
-                    ok = mbar_wait(&bars->y_full[st], (n >> 1) & 1, abort_flag, dev_status);
-                    if (!ok) break;
-                    int y_head, y_row;
-                    inner_step<KEYMAJOR, GEN, SINK>(it, o, s, G, y_head, y_row);
-                    const int rows = it.doc_end - y_row;  // rows of the document
-                    if (rows < kBlockN) {
-                        uint8_t* y = smem + L::kOffY + st * 2 * L::kTile;
-                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                        // a row is 128 bytes of each 64-column chunk (the swizzle stays inside them)
-                        for (int x = at; x < (kBlockN - rows) * 8; x += 64)
-#pragma unroll
-                            for (int c = 0; c < 2 * HD / 64; ++c)
-                                *reinterpret_cast<uint4*>(y + c * L::kChunk + rows * 128 + x * 16) = z;
-                        fence_proxy_async_smem();
-                    }
-                    mbar_arrive(&bars->y_ok[st]);
-                }
-            }
-        }
+        // ------------------------------------------------------------ idle (register split only)
     } else if (warp == 8) {
         // ------------------------------------------------------------ producer
         // Per outer tile: with reuse its new Y fills, then X (the order in which their slots are
@@ -346,7 +291,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                                                    abort_flag, dev_status)))
                 return false;
             int y_head, y_row;
-            inner_step<KEYMAJOR, GEN, SINK>(it, o, s, G, y_head, y_row);
+            inner_step<KEYMAJOR, GEN>(it, o, s, G, y_head, y_row);
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars->y_full[st], 2 * L::kTile);
                 uint8_t* y = smem + L::kOffY + st * 2 * L::kTile;
@@ -377,8 +322,8 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
             const BandItem it = decode_band(wk.cur);
             if (!item_used<KEYMAJOR>(it, G)) continue;
             const int x_head = KEYMAJOR ? it.head / G : it.head;
-            for (int u = 0; ok && u < (SINK ? 1 : it.n_qt); ++u) {
-                const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, u, G, p);
+            for (int u = 0; ok && u < it.n_qt; ++u) {
+                const OuterTile o = outer_tile<KEYMAJOR, GEN>(it, u, G, p);
                 for (int s = 0; ok && reuse && s < o.n_sub; ++s) {
                     const StepFill f = ft.step(true, u, it.n_qt, s, o.n_sub);
                     if (f.first) ok = load_y(it, o, s, f.idx);
@@ -421,154 +366,71 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
             FillTrack<KEYMAJOR> ft;
             bool ok = true;
             ItemWalk wk;
-            if constexpr (SINK) {
-                // The two halves of a step run half a step apart, each with its own S and dP products (N =
-                // 64): while one warpgroup is at its elementwise work the other half's products run.
-                // (Both halves at once, as below, leave the tensor cores idle meanwhile: dQ 675, dK / dV 798
-                // us against 548 and 643 for 2 x 8192 tokens, 32 / 8 heads of 128, window 1024.)
-                uint32_t n[2] = {0, 0};  // steps of half h whose S and dP products are issued
-                struct Second {          // the second products of half 1 still to issue
-                    bool on, first, last;
-                    uint32_t st, cols;
-                } later{false, false, false, 0, 0};
-                constexpr int kHalf = kBlockN / 2;
-                auto first_products = [&](int h, uint32_t st, uint32_t cols) {
-                    if (n[h] > 0)
-                        ok = mbar_wait(&bars->m2_done[h], (n[h] - 1) & 1, abort_flag, dev_status);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile + h * kHalf * 128, y1 = y0 + L::kTile;
-                    const uint32_t id = (idesc1 & ~(0x3Fu << 17)) | ((cols >> 3) << 17);
-                    const uint64_t dx0 = desc_kmajor(x0, 0), dx1 = desc_kmajor(x1, 0);
-                    const uint64_t dy0 = desc_kmajor(y0, 0), dy1 = desc_kmajor(y1, 0);
-                    if (cols > 0)
-#pragma unroll
-                        for (int kk = 0; kk < HD / 16; ++kk) {  // (as desc_kmajor steps)
-                            const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                            umma_f16_ss(tm_s + kHalf * h, dx0 + step, dy0 + step, id, kk == 0 ? 0u : 1u);
-                            umma_f16_ss(tm_dp + kHalf * h, dx1 + step, dy1 + step, id, kk == 0 ? 0u : 1u);
-                        }
-                    umma_commit(&bars->s_full[h]);
-                    ++n[h];
-                };
-                auto second_products = [&](int h, uint32_t st, uint32_t cols, bool first) {
-                    ok = mbar_wait(&bars->p_full[h], (n[h] - 1) & 1, abort_flag, dev_status);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile, y1 = y0 + L::kTile;
-                    const uint64_t dy0 = desc_v(y0, 4 * h), dy1 = desc_v(y1, 4 * h);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t acc = (!first || h > 0 || kk > 0) ? 1u : 0u;
-                        if (static_cast<uint32_t>(16 * kk) >= cols) continue;
-                        umma_f16_ts(tm_acc_ds, tm_dp + kHalf * h + 8 * kk, dy0 + kk * (2048 >> 4), idesc2, acc);
-                        if (KEYMAJOR)
-                            umma_f16_ts(tm_acc_p, tm_s + kHalf * h + 8 * kk, dy1 + kk * (2048 >> 4), idesc2, acc);
+            for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
+                if (!wk.has()) continue;
+                const BandItem it = decode_band(wk.cur);
+                if (!item_used<KEYMAJOR>(it, G)) continue;
+                for (int u = 0; ok && u < it.n_qt; ++u) {
+                    const OuterTile o = outer_tile<KEYMAJOR, GEN>(it, u, G, p);
+                    if (!mbar_wait(&bars->x_full, oc & 1, abort_flag, dev_status)) {
+                        ok = false;
+                        break;
                     }
-                    umma_commit(&bars->m2_done[h]);
-                };
-                auto finish_later = [&]() {
-                    if (!later.on) return;
-                    later.on = false;
-                    second_products(1, later.st, later.cols, later.first);
-                    if (!ok) return;
-                    umma_commit(&bars->y_empty[later.st]);
-                    if (later.last) umma_commit(&bars->acc_full);
-                };
-                uint32_t fill = 0;  // every step has its own fill
-                for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
-                    if (!wk.has()) continue;
-                    const BandItem it = decode_band(wk.cur);
-                    const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, 0, G, p);
-                    for (int s = 0; ok && s < o.n_sub; ++s, ++fill) {
-                        const uint32_t st = fill & 1;
-                        // a step over the sinks alone takes their columns only (whole K = 16 slices)
-                        const uint32_t all = !KEYMAJOR && o.sink0 && s == 0 ? (p.sinks + 15) & ~15 : kBlockN;
-                        const uint32_t c0 = all < kHalf ? all : kHalf, c1 = all - c0;
-                        if (s == 0) {
-                            finish_later();  // before the wait for X: the last tile's epilogue waits for it
-                            ok = ok && mbar_wait(&bars->x_full, oc & 1, abort_flag, dev_status);
-                        }
-                        ok = ok && mbar_wait(&bars->y_ok[st], (fill >> 1) & 1, abort_flag, dev_status);
-                        if (ok) first_products(0, st, c0);
-                        if (ok) finish_later();
-                        if (ok) first_products(1, st, c1);
-                        if (!ok) break;
-                        if (s + 1 == o.n_sub) umma_commit(&bars->x_empty);
-                        if (s == 0 && oc > 0) ok = mbar_wait(&bars->acc_empty, (oc - 1) & 1, abort_flag, dev_status);
-                        if (ok) second_products(0, st, c0, s == 0);
-                        later = {true, s == 0, s + 1 == o.n_sub, st, c1};
-                    }
-                    ++oc;
-                }
-                if (ok) finish_later();
-            } else {
-                for (wk.start(items, n_items, KEYMAJOR ? G : 1, H); ok && !wk.done(); wk.advance()) {
-                    if (!wk.has()) continue;
-                    const BandItem it = decode_band(wk.cur);
-                    if (!item_used<KEYMAJOR>(it, G)) continue;
-                    for (int u = 0; ok && u < it.n_qt; ++u) {
-                        const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, u, G, p);
-                        if (!mbar_wait(&bars->x_full, oc & 1, abort_flag, dev_status)) {
+                    for (int s = 0; s < o.n_sub; ++s) {
+                        const StepFill f = ft.step(reuse, u, it.n_qt, s, o.n_sub);
+                        const uint32_t st = f.idx & 1;
+                        const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile, y1 = y0 + L::kTile;
+                        // each fill is waited for once, by its first reader, in fill order
+                        if (f.first &&
+                            !mbar_wait(&bars->y_full[st], (f.idx >> 1) & 1, abort_flag, dev_status)) {
                             ok = false;
                             break;
                         }
-                        for (int s = 0; s < o.n_sub; ++s) {
-                            const StepFill f = ft.step(reuse, u, it.n_qt, s, o.n_sub);
-                            const uint32_t st = f.idx & 1;
-                            const uint32_t y0 = sbase + L::kOffY + st * 2 * L::kTile, y1 = y0 + L::kTile;
-                            // each fill is waited for once, by its first reader, in fill order
-                            if (f.first &&
-                                !mbar_wait(&bars->y_full[st], (f.idx >> 1) & 1, abort_flag, dev_status)) {
+                        // S = X0 Y0^T and dP = X1 Y1^T at full width (N = 128); their columns are free
+                        // once the previous step's second products of both halves are done
+                        for (int h = 0; ok && h < 2; ++h)
+                            if (sc > 0 && !mbar_wait(&bars->m2_done[h], (sc - 1) & 1, abort_flag,
+                                                     dev_status))
+                                ok = false;
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < HD / 16; ++kk) {
+                            umma_f16_ss(tm_s, desc_kmajor(x0, kk), desc_kmajor(y0, kk), idesc1,
+                                        kk == 0 ? 0u : 1u);
+                            umma_f16_ss(tm_dp, desc_kmajor(x1, kk), desc_kmajor(y1, kk), idesc1,
+                                        kk == 0 ? 0u : 1u);
+                        }
+                        umma_commit(&bars->s_full[0]);  // one per elementwise warpgroup
+                        umma_commit(&bars->s_full[1]);
+                        if (!ok) break;
+                        if (s + 1 == o.n_sub) umma_commit(&bars->x_empty);
+                        // second products of half h: K = the half's 64 Y rows
+                        for (int h = 0; ok && h < 2; ++h) {
+                            if (!mbar_wait(&bars->p_full[h], sc & 1, abort_flag, dev_status) ||
+                                (s == 0 && h == 0 && oc > 0 &&
+                                 !mbar_wait(&bars->acc_empty, (oc - 1) & 1, abort_flag, dev_status))) {
                                 ok = false;
                                 break;
                             }
-                            // S = X0 Y0^T and dP = X1 Y1^T at full width (N = 128); their columns are free
-                            // once the previous step's second products of both halves are done
-                            for (int h = 0; ok && h < 2; ++h)
-                                if (sc > 0 && !mbar_wait(&bars->m2_done[h], (sc - 1) & 1, abort_flag,
-                                                         dev_status))
-                                    ok = false;
-                            if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int kk = 0; kk < HD / 16; ++kk) {
-                                umma_f16_ss(tm_s, desc_kmajor(x0, kk), desc_kmajor(y0, kk), idesc1,
-                                            kk == 0 ? 0u : 1u);
-                                umma_f16_ss(tm_dp, desc_kmajor(x1, kk), desc_kmajor(y1, kk), idesc1,
-                                            kk == 0 ? 0u : 1u);
-                            }
-                            umma_commit(&bars->s_full[0]);  // one per elementwise warpgroup
-                            umma_commit(&bars->s_full[1]);
-                            if (!ok) break;
-                            if (s + 1 == o.n_sub) umma_commit(&bars->x_empty);
-                            // second products of half h: K = the half's 64 Y rows
-                            for (int h = 0; ok && h < 2; ++h) {
-                                if (!mbar_wait(&bars->p_full[h], sc & 1, abort_flag, dev_status) ||
-                                    (s == 0 && h == 0 && oc > 0 &&
-                                     !mbar_wait(&bars->acc_empty, (oc - 1) & 1, abort_flag, dev_status))) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    const uint32_t acc = (s > 0 || h > 0 || kk > 0) ? 1u : 0u;
-                                    umma_f16_ts(tm_acc_ds, tm_dp + 64 * h + 8 * kk, desc_v(y0, 4 * h + kk),
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint32_t acc = (s > 0 || h > 0 || kk > 0) ? 1u : 0u;
+                                umma_f16_ts(tm_acc_ds, tm_dp + 64 * h + 8 * kk, desc_v(y0, 4 * h + kk),
+                                            idesc2, acc);
+                                if (KEYMAJOR)
+                                    umma_f16_ts(tm_acc_p, tm_s + 64 * h + 8 * kk, desc_v(y1, 4 * h + kk),
                                                 idesc2, acc);
-                                    if (KEYMAJOR)
-                                        umma_f16_ts(tm_acc_p, tm_s + 64 * h + 8 * kk, desc_v(y1, 4 * h + kk),
-                                                    idesc2, acc);
-                                }
-                                umma_commit(&bars->m2_done[h]);
                             }
-                            if (!ok) break;
-                            if (f.last) umma_commit(&bars->y_empty[st]);
-                            if (s + 1 == o.n_sub) umma_commit(&bars->acc_full);
-                            ++sc;
+                            umma_commit(&bars->m2_done[h]);
                         }
-                        ++oc;
+                        if (!ok) break;
+                        if (f.last) umma_commit(&bars->y_empty[st]);
+                        if (s + 1 == o.n_sub) umma_commit(&bars->acc_full);
+                        ++sc;
                     }
+                    ++oc;
                 }
             }
             // Wait (bounded) until every MMA this thread issued has finished.
@@ -593,8 +455,8 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
             if (!wk.has()) continue;
             const BandItem it = decode_band(wk.cur);
             if (!item_used<KEYMAJOR>(it, G)) continue;
-            for (int u = 0; ok && u < (SINK ? 1 : it.n_qt); ++u) {
-                const OuterTile o = outer_tile<KEYMAJOR, GEN, SINK>(it, u, G, p);
+            for (int u = 0; ok && u < it.n_qt; ++u) {
+                const OuterTile o = outer_tile<KEYMAJOR, GEN>(it, u, G, p);
                 const int slot = o.row0 + row;  // key slot (key-major) or query slot
                 const bool valid = slot < it.doc_end;
                 float lse2 = 0.f, dd = 0.f;  // query-major: this row's lse * log2(e) and D
@@ -607,22 +469,19 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                     const StepFill f = ft.step(reuse, u, it.n_qt, s, o.n_sub);
                     const uint32_t st = f.idx & 1;
                     int y_head, y_row;
-                    inner_step<KEYMAJOR, GEN, SINK>(it, o, s, G, y_head, y_row);
+                    inner_step<KEYMAJOR, GEN>(it, o, s, G, y_head, y_row);
                     // visible columns [c_lo, c_hi] of this row
                     int c_lo, c_hi;
-                    int c_sk = 0;  // SINK, query-major: columns below it are sinks
                     if (GEN) {
                         const int a = it.doc_start, b = it.doc_end;
                         if (KEYMAJOR) {  // the queries that see key `slot`
-                            const bool all = SINK && slot - a < p.sinks;
                             c_lo = (p.causal ? slot : a) - y_row;
-                            c_hi = ((p.causal && window > 0 && !all) ? min(slot + window - 1, b - 1) : b - 1) - y_row;
+                            c_hi = ((p.causal && window > 0) ? min(slot + window - 1, b - 1) : b - 1) - y_row;
                         } else {         // the keys query `slot` sees
                             c_lo = ((window > 0) ? max(a, slot - window + 1) : a) - y_row;
                             c_hi = (p.causal ? slot : b - 1) - y_row;
-                            if (SINK) c_sk = a + p.sinks - y_row;
                         }
-                        if (!valid) c_hi = SINK ? -1 : c_lo - 1;
+                        if (!valid) c_hi = c_lo - 1;
                     } else if (KEYMAJOR) {  // queries slot .. slot + window - 1, inside the document
                         c_lo = slot - y_row;
                         c_hi = min(slot + window - 1, it.doc_end - 1) - y_row;
@@ -636,17 +495,14 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->y_full[st], (f.idx >> 1) & 1,
                                                                abort_flag, dev_status));
                     if (!ok) break;
+                    const int w_lo = __reduce_min_sync(0xffffffffu, c_lo);
+                    const int w_hi = __reduce_max_sync(0xffffffffu, c_hi);
                     const float* l2v = vec + st * 256;
                     {
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[h], sc & 1, abort_flag,
                                                                dev_status));
                         if (!ok) break;
                         tc_fence_after();
-                        // what nobody reads is left out: columns behind the sinks' slices in a step over
-                        // them alone, rows that are no sinks in a far piece (their sums are not kept)
-                        const int n_cols = SINK && !KEYMAJOR && o.sink0 && s == 0 ? (p.sinks + 15) & ~15 : kBlockN;
-                        const bool idle = SINK && (64 * h >= n_cols || (KEYMAJOR && o.piece >= 0 && r0 >= p.sinks));
-                        if (!idle) {
                         // the half's 64 columns of S and dP, one wait
                         uint32_t sv[64], dv[64];
 #pragma unroll
@@ -663,12 +519,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
 #pragma unroll
                         for (int cc = 0; cc < 2; ++cc) {
                             const int c = 2 * h + cc;
-                            if (SINK && 32 * c >= n_cols) continue;
                             uint32_t pk[16], dk[16];
-                            // SINK: bit e = column 32 c + e is visible
-                            const uint32_t bits = SINK ? low_bits(c_hi + 1 - 32 * c) &
-                                                             (~low_bits(c_lo - 32 * c) | low_bits(c_sk - 32 * c))
-                                                       : 0u;
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 // key-major: the four columns' lse * log2(e) and D, one broadcast
@@ -684,13 +535,9 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
 #pragma unroll
                                 for (int x = 0; x < 4; ++x) {
                                     const int col = 32 * c + e + x;
+                                    const bool vis = col >= c_lo && col <= c_hi;
                                     const float pe = ex2(fmaf(__uint_as_float(sv[32 * cc + e + x]), scale_log2, -l2q[x]));
-                                    if (SINK) {
-                                        pr[x] = ((bits >> (e + x)) & 1u) ? pe : 0.f;
-                                    } else {
-                                        const bool vis = col >= c_lo && col <= c_hi;
-                                        pr[x] = vis ? pe : 0.f;
-                                    }
+                                    pr[x] = vis ? pe : 0.f;
                                     dr[x] = pr[x] * (__uint_as_float(dv[32 * cc + e + x]) - dq4[x]);
                                 }
                                 pk[e >> 1] = pack_bf16x2(pr[0], pr[1]);
@@ -702,7 +549,6 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                             // columns of this half already read
                             if (KEYMAJOR) tmem_st16(tm_lane + L::kTmS + 16 * c + 32 * h, pk);
                             tmem_st16(tm_lane + L::kTmDP + 16 * c + 32 * h, dk);
-                        }
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -721,45 +567,10 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                 const int out_heads = KEYMAJOR ? Hkv : H;
                 const int out_head = KEYMAJOR ? it.head / G : it.head;
                 const int64_t base = (static_cast<int64_t>(slot) * out_heads + out_head) * HD;
-                bool store = true;  // rows of dQ, dK, dV in bf16
-                if (KEYMAJOR && SINK && p.sinks > 0 && p.window > 0 && o.row0 == it.doc_start) {
-                    // key tile 0: where the document has far query tiles, the sinks' rows of this part
-                    const int64_t slots = it.doc_end - it.doc_start;
-                    const int far = sink_far_tile(p.window, slots);
-                    if (far * static_cast<int64_t>(kBlockN) < slots) {
-                        store = o.piece < 0;
-                        int d = -1, z = p.batch;  // the document: last one that starts at or before
-                        while (z - d > 1) {
-                            const int mid = (d + z) >> 1;
-                            if (static_cast<int64_t>(p.cu_seqlens[mid]) * p.slot_mult <= it.doc_start) d = mid; else z = mid;
-                        }
-                        const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
-                        const int64_t q_first = it.doc_start + static_cast<int64_t>(far + o.piece * c) * kBlockN;
-                        const int64_t part = o.piece < 0 ? d : p.batch + d + q_first / (static_cast<int64_t>(c) * kBlockN);
-                        float* dst = p.sink_part + ((part * Hkv + out_head) * p.sinks + row) * 2 * HD;
-#pragma unroll 1
-                        for (int a = 0; a < 2; ++a) {
-#pragma unroll 1
-                            for (int cc = h * (HD / 64); cc < (h + 1) * (HD / 64); ++cc) {
-                                uint32_t v[32];
-                                tmem_ld32(tm_lane + L::kTmAcc + (a == 0 ? HD : 0) + 32 * cc, v);
-                                tmem_wait_ld();
-                                regs_after_wait(v);
-                                const float mul = a == 0 ? p.scale : 1.f;
-                                if (row < p.sinks)
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 4)
-                                        *reinterpret_cast<float4*>(dst + a * HD + 32 * cc + e) =
-                                            make_float4(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul,
-                                                        __uint_as_float(v[e + 2]) * mul, __uint_as_float(v[e + 3]) * mul);
-                            }
-                        }
-                    }
-                }
                 // key-major with hd 128, a warp whose 32 rows all lie inside the document: its
                 // rows of dK (times scale), then of dV (this warpgroup's 64 columns) go out
                 // through its 2 KB staging box, 16 rows (one TMA store) at a time
-                const bool tma_km = store && KEYMAJOR && HD == 128 && o.row0 + r0 + 31 < it.doc_end;
+                const bool tma_km = KEYMAJOR && HD == 128 && o.row0 + r0 + 31 < it.doc_end;
                 if (tma_km) {
                     uint8_t* stg = smem + L::kOffStg + warp * 2048;
 #pragma unroll 1
@@ -806,7 +617,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
                 // and written by one TMA store; otherwise every thread stores its own row
                 const bool tma_rows = !KEYMAJOR && HD == 128 && o.row0 + r0 + 31 < it.doc_end;
 #pragma unroll 1
-                for (int a = 0; store && !tma_km && a < (KEYMAJOR ? 2 : 1); ++a) {
+                for (int a = 0; !tma_km && a < (KEYMAJOR ? 2 : 1); ++a) {
                     // a = 0: the dS product (dQ or dK, times scale); a = 1: dV
                     const uint32_t col0 = L::kTmAcc + (KEYMAJOR && a == 0 ? HD : 0);
                     const float mul = a == 0 ? p.scale : 1.f;
@@ -859,54 +670,22 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, L::kTmemCols);
 }
 
-// Block (document, kv head, 256 of the values): the sinks' rows of dk, dv of documents with far query
-// tiles, summed over the window's part and the pieces in order.
-__global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProblem p, __nv_bfloat16* dk,
-                                                                __nv_bfloat16* dv, const WorkspaceHeader* hdr) {
-    if (hdr->status != DEV_OK) return;
-    const int d = blockIdx.x, g = blockIdx.y, hd = p.head_dim;
-    const int64_t a = static_cast<int64_t>(p.cu_seqlens[d]) * p.slot_mult;
-    const int64_t slots = static_cast<int64_t>(p.cu_seqlens[d + 1]) * p.slot_mult - a;
-    if (slots == 0) return;
-    const int far = sink_far_tile(p.window, slots);
-    const int n_far = static_cast<int>((slots + kBlockN - 1) / kBlockN) - far;
-    if (n_far <= 0) return;
-    const int c = sink_piece_tiles(p.window, p.max_len, p.slot_mult);
-    const int pieces = (n_far + c - 1) / c;
-    // pieces start exactly one piece apart: consecutive places
-    const int64_t place = p.batch + d + (a + static_cast<int64_t>(far) * kBlockN) / (static_cast<int64_t>(c) * kBlockN);
-    const int width = p.sinks * 2 * hd;
-    const int64_t stride = static_cast<int64_t>(p.kv_heads) * width;
-    const float* first = p.sink_part + (static_cast<int64_t>(d) * p.kv_heads + g) * width;
-    const float* rest = p.sink_part + (place * p.kv_heads + g) * width;
-    const int x = blockIdx.z * 256 + threadIdx.x;
-    if (x < width) {
-        float sum = first[x];
-#pragma unroll 8
-        for (int f = 0; f < pieces; ++f) sum += rest[f * stride + x];
-        const int m = x / (2 * hd), e = x % (2 * hd);  // (a document with far tiles has more than `sinks` rows)
-        const int64_t row = ((a + m) * p.kv_heads + g) * hd;
-        if (e < hd) dk[row + e] = __float2bfloat16_rn(sum);
-        else dv[row + e - hd] = __float2bfloat16_rn(sum);
-    }
-}
-
-template <int HD, bool KEYMAJOR, bool GEN, bool SINK>
+template <int HD, bool KEYMAJOR, bool GEN>
 cudaError_t launch_bwd_tc_one(const AttnProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const CUtensorMap& tdo,
                               const CUtensorMap& tst, const CUtensorMap& tst2, const float* dsum,
                               __nv_bfloat16* out_a, __nv_bfloat16* out_b, const int4* items,
                               WorkspaceHeader* hdr, int sms, cudaStream_t stream) {
     using L = BwdLayout<HD, KEYMAJOR>;
-    cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<HD, KEYMAJOR, GEN, SINK>,
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<HD, KEYMAJOR, GEN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
-    attn_bwd_tc_kernel<HD, KEYMAJOR, GEN, SINK><<<sms, kBwdTcThreads, L::kSmemBytes, stream>>>(
+    attn_bwd_tc_kernel<HD, KEYMAJOR, GEN><<<sms, kBwdTcThreads, L::kSmemBytes, stream>>>(
         tq, tk, tv, tdo, tst, tst2, p, dsum, out_a, out_b, items, hdr);
     return cudaGetLastError();
 }
 
-template <int HD, bool GEN, bool SINK = false>
+template <int HD, bool GEN>
 cudaError_t launch_bwd_tc_hd(const AttnProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, const CUtensorMap& tdo,
                              const CUtensorMap& tdq, const CUtensorMap& tdk,
@@ -919,12 +698,12 @@ cudaError_t launch_bwd_tc_hd(const AttnProblem& p, const CUtensorMap& tq, const 
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     if ((which & 1) &&
-        (e = launch_bwd_tc_one<HD, false, GEN, SINK>(p, tq, tk, tv, tdo, tdq, tdq, dsum,
+        (e = launch_bwd_tc_one<HD, false, GEN>(p, tq, tk, tv, tdo, tdq, tdq, dsum,
                                                static_cast<__nv_bfloat16*>(dq), nullptr, items, hdr,
                                                sms, stream)) != cudaSuccess)
         return e;
     if (which & 2)
-        return launch_bwd_tc_one<HD, true, GEN, SINK>(p, tq, tk, tv, tdo, tdk, tdv, dsum,
+        return launch_bwd_tc_one<HD, true, GEN>(p, tq, tk, tv, tdo, tdk, tdv, dsum,
                                                 static_cast<__nv_bfloat16*>(dk),
                                                 static_cast<__nv_bfloat16*>(dv), items, hdr, sms,
                                                 stream);
@@ -938,13 +717,7 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
                                const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
                                const CUtensorMap& tm_dk, const CUtensorMap& tm_dv,
                                const float* dsum, void* dq, void* dk, void* dv, const int4* items,
-                               WorkspaceHeader* hdr, int which, cudaStream_t stream, bool sinks) {
-    if (sinks && p.head_dim == 128)
-        return launch_bwd_tc_hd<128, true, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dk, tm_dv, dsum, dq, dk, dv,
-                                                 items, hdr, which, stream);
-    if (sinks && p.head_dim == 64)
-        return launch_bwd_tc_hd<64, true, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dk, tm_dv, dsum, dq, dk, dv,
-                                                items, hdr, which, stream);
+                               WorkspaceHeader* hdr, int which, cudaStream_t stream) {
     const bool band = band_applies(p);
     if (p.head_dim == 128)
         return band ? launch_bwd_tc_hd<128, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dk, tm_dv, dsum, dq,
@@ -957,13 +730,6 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
                     : launch_bwd_tc_hd<64, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dk, tm_dv, dsum, dq,
                                                  dk, dv, items, hdr, which, stream);
     return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_attn_bwd_sink_sum(const AttnProblem& p, void* dk, void* dv,
-                                     const WorkspaceHeader* hdr, cudaStream_t stream) {
-    attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads, (p.sinks * 2 * p.head_dim + 255) / 256), 256, 0, stream>>>(
-        p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr);
-    return cudaGetLastError();
 }
 
 }  // namespace pha

@@ -177,12 +177,22 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
                                const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
                                const CUtensorMap& tm_dk, const CUtensorMap& tm_dv,
                                const float* dsum, void* dq, void* dk, void* dv, const int4* items,
-                               WorkspaceHeader* hdr, int which, cudaStream_t stream,
-                               bool sinks = false);
+                               WorkspaceHeader* hdr, int which, cudaStream_t stream);
 
-// Sum of the sinks' dk, dv over the far pieces of each document (p.sink_part), into dk, dv (bf16).
-cudaError_t launch_attn_bwd_sink_sum(const AttnProblem& p, void* dk, void* dv,
-                                     const WorkspaceHeader* hdr, cudaStream_t stream);
+// Backward with window and sinks (bf16, head_dim 64 / 128; p.sinks, p.window may be 0): dQ over a
+// kSchedTilesQ list, dK / dV over a kSchedTilesK list (with far pieces, summed at the end). Maps as
+// launch_attn_bwd_tc.
+cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm_q,
+                                     const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                     const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
+                                     const float* dsum, void* dq, const int4* items,
+                                     WorkspaceHeader* hdr, cudaStream_t stream);
+cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& tm_q,
+                                       const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                       const CUtensorMap& tm_do, const CUtensorMap& tm_dk,
+                                       const CUtensorMap& tm_dv, const float* dsum, void* dk,
+                                       void* dv, const int4* items, WorkspaceHeader* hdr,
+                                       cudaStream_t stream);
 
 // RoPE preceded by the QK RMS-norm of every head row (weights may be NULL = ones).
 cudaError_t launch_qk_norm_rope(void* q, void* k, const float* q_weight, const float* k_weight,

@@ -232,13 +232,10 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
         !encode_slot_map(&tdv, dv, wk, rows, 16))
         return PHA_ERR_CUDA;
     if (launch_attn_bwd_zero_outside(p, dq, dk, dv, stream) != cudaSuccess ||
-        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, list(0), hdr, 1, stream, true) !=
-            cudaSuccess ||
-        build(kSchedTilesK, w.keys, w.items_k) != cudaSuccess ||
-        launch_attn_bwd_tc(p, tq, tk, tv, tdo, tdq, tdk, tdv, dsum, dq, dk, dv, list(w.keys), hdr_k, 2, stream,
-                           true) != cudaSuccess)
+        launch_attn_bwd_sinks_dq(p, tq, tk, tv, tdo, tdq, dsum, dq, list(0), hdr, stream) != cudaSuccess ||
+        build(kSchedTilesK, w.keys, w.items_k) != cudaSuccess)
         return PHA_ERR_CUDA;
-    return p.sinks > 0 ? of(launch_attn_bwd_sink_sum(p, dk, dv, hdr, stream)) : PHA_OK;
+    return of(launch_attn_bwd_sinks_dkdv(p, tq, tk, tv, tdo, tdk, tdv, dsum, dk, dv, list(w.keys), hdr_k, stream));
 }
 
 }  // extern "C"
