@@ -16,14 +16,16 @@
 // attn_bwd_sink_sum_kernel; so no CTA walks a whole document, and no atomics are used.
 //
 // What bounds it: the S and dP products read both operands from shared memory (128 bytes a clock: 64
-// clocks for each K = 16 slice of a 128 x 128 product, twice its tensor time), the others one; with 16
-// + 16 slices that is about 1,500 clocks a step (key-major), to which the chain S -> P -> dV -> S of
+// clocks for each K = 16 slice of a 128 x 128 product), the others one; with 16 + 16 slices that is about
+// 2,050 clocks a step (key-major; 1,540 query-major), to which the chain S -> P -> dV -> S of
 // one step must not add up. So the elementwise work is cut in two, P from S (stage A) and dS from dP
 // (stage B), and each overlaps the other's products: while stage B runs, dV += P^T dO and the next S
 // are computed; while the next stage A runs, dK += dS^T Q and the next dP. (Both stages after both
 // products, as in attn_bwd_tc.cu: 798 us for dK / dV of 2 x 8192 tokens, 32 / 8 heads of 128, window
 // 1024, 675 for dQ; the two column halves of a step staggered instead: 680 and 574, the halves' N = 64
-// products reading X twice.)
+// products reading X twice; this one: 603 and 441, 4,200 and 3,000 clocks a step.) What is left over the
+// products' 2,050 and 1,540 clocks is the chain S -> P -> dV -> next S, P lying in S's columns: with 256
+// columns of accumulators TMEM has no room for a second S.
 // TMEM columns: S [0, 128), dP [128, 256), accumulators from 256 (dV, dK or dQ). Key-major, P^T and dS^T
 // of column half h (bf16 A operands) overwrite the first 32 of the half's own S or dP columns;
 // query-major, dS goes to two buffers of 64 columns at 384 so that S and dP of the next step wait only
@@ -32,10 +34,12 @@
 // CTA = 12 warps, one per SM, persistent over the list (items dealt in snake order):
 //   warps 0-7   two warpgroups, warpgroup h taking columns 64 h .. 64 h + 63 of every step (row = TMEM
 //               lane) and half h of the accumulator columns in the epilogue
-//   warp 8      producer (TMA; key-major also lse log2(e) and D of the fill's queries)
-//   warp 9      MMA issuer, owner of the 512 TMEM columns
-//   warps 10-11 blank the rows of each landed Y tile that lie behind the document's end: whatever is there
-//               (a padded batch's NaN) would meet a zero weight, and 0 * NaN is NaN
+//   warp 8      issues the second products (dV and dK, or dQ)
+//   warp 9      issues the first products (S and dP); owner of the 512 TMEM columns. (One thread for all
+//               four products spent 2,500 of 5,200 clocks a step between them.)
+//   warp 10     producer: X and Y tiles by TMA, key-major also -lse log2(e) and -D of the queries
+//   warp 11     blanks the rows of a landed Y tile that lie behind the document's end: whatever is there (a
+//               padded batch's NaN) would meet a zero weight, and 0 * NaN is NaN
 // Every wait is bounded (1 s); on expiry the CTA records a status, drains its own copies and MMAs,
 // frees TMEM and exits.
 #include <cuda.h>
@@ -59,32 +63,58 @@ template <int HD, bool KEYMAJOR>
 struct Layout {
     static constexpr int kChunk = 128 * 128;  // one [128 rows][64 bf16] swizzled chunk (bytes)
     static constexpr int kTile = 128 * HD * 2;
+    // Buffers of Y0 and of Y1. Y0 (Q or K) is read until the step's last product and wanted first by the
+    // next but one's S; Y1 (dO or V) is wanted last and done with early: with two of each, Y0 came too
+    // late (1,500 clocks a step).
+    static constexpr int kR0 = 3, kR1 = 1;
     static constexpr int kOffX = 0;                        // X0, X1
-    static constexpr int kOffY = kOffX + 2 * kTile;        // [2 stages] Y0, Y1
-    // key-major: [2 stages] lse2[128], D[128]; then 2 KB per warp (a 16-row box of dK / dV on its way
+    static constexpr int kOffY0 = kOffX + 2 * kTile;
+    static constexpr int kOffY1 = kOffY0 + kR0 * kTile;
+    // key-major: per Y0 buffer -lse2[128], -D[128]; then 2 KB per warp (a 16-row box of dK / dV on its way
     // out); query-major: the dQ tile on its way out
-    static constexpr int kOffVec = kOffY + 4 * kTile;
-    static constexpr int kOffStg = kOffVec + (KEYMAJOR ? 2 * 2 * 128 * 4 : 0);
+    static constexpr int kOffVec = kOffY1 + kR1 * kTile;
+    static constexpr int kOffStg = kOffVec + (KEYMAJOR ? kR0 * 2 * 128 * 4 : 0);
     static constexpr int kOffBar = kOffStg + (KEYMAJOR ? 8 * 2048 : kTile);
-    static constexpr int kBarBytes = 256;
+    static constexpr int kBarBytes = 512;
     static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + slack to align to 1024
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kTmS = 0, kTmDP = 128, kTmAcc = 256, kTmDS = 384;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
+// What the producer tells the other roles, in shared memory: of each step, with its Y0 tile (read after
+// y0_full or y0_ok), and of each outer tile (four of them: a step three before a tile's first one belongs
+// at the latest to the tile three before it, so everybody has left the one four before). The other roles
+// decode nothing: their code has to stay small beside the elementwise loops, whose instructions it pushes
+// out of the cache (each role walking the list by itself: 656 us instead of 603 for dK / dV, 496 instead
+// of 441 for dQ, 2 x 8192 tokens, 32 / 8 heads of 128, window 1024).
+struct StepRec {
+    int flags;  // kFirst, kLast step of its outer tile; kEnd: no step, the list is done
+    int y_row;  // first slot of the Y tiles
+    int rows;   // rows of them inside the document
+    int cols;   // columns that are multiplied
+};
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
+struct TileRec {
+    int row0, head, doc_start, doc_end, piece;
+};
+
 struct Bars {
     uint64_t x_full, x_empty;
-    uint64_t y_full[2], y_ok[2], y_empty[2];
+    uint64_t y0_full[3], y0_ok[3], y0_empty[3];
+    uint64_t y1_full, y1_ok, y1_empty;
+    uint64_t vec_full[3];       // key-major: -lse2 and -D of the queries
     uint64_t s_full, dp_full;   // a step's S / dP are in TMEM
     uint64_t a_done, b_done;    // stage A / B done by both warpgroups (key-major: P / dS stored; query-major,
                                 // a_done: S read, b_done: dS stored)
     uint64_t dp_read;           // query-major: dP read
-    uint64_t m2a_done;          // key-major: dV product complete (P's columns are free)
-    uint64_t m2b_done[2];       // dK product complete (key-major: [0]) or dQ's of dS buffer i
-    uint64_t acc_full, acc_empty, drain;
+    uint64_t m2_done[2];        // key-major: dV's / dK's product complete (P's / dS's columns are free);
+                                // query-major: dQ's of dS buffer i
+    uint64_t acc_full, acc_empty, drain[2];
     uint32_t tmem_base;
     int abort;
+    StepRec step[3];
+    TileRec tile[4];
 };
 
 // The low n bits (n clamped to 0 .. 32).
@@ -156,6 +186,18 @@ __device__ __forceinline__ void step_tile(const Tile& o, int s, int G, int& y_he
     }
 }
 
+// Place in a ring of N buffers, and the parity of its lap.
+template <int N>
+struct Ring {
+    uint32_t i = 0, lap = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            lap ^= 1;
+        }
+    }
+};
+
 // Columns of step s that are multiplied.
 template <bool KEYMAJOR>
 __device__ __forceinline__ int step_cols(const Tile& o, int s, const AttnProblem& p) {
@@ -167,12 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_sinks_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                           const __grid_constant__ CUtensorMap tm_st, const __grid_constant__ CUtensorMap tm_st2,
-                          const AttnProblem p, const float* __restrict__ dsum, __nv_bfloat16* __restrict__ out_a,
+                          const AttnProblem p, const float* __restrict__ nlse, const float* __restrict__ nd,
+                          __nv_bfloat16* __restrict__ out_a,
                           __nv_bfloat16* __restrict__ out_b, const int4* __restrict__ items, WorkspaceHeader* hdr) {
     // out_a: dQ (query-major) or dK (key-major); out_b: dV (key-major); tm_st: a map over dQ with a 64 x
     // 32 box or over dK with a 64 x 16 box; tm_st2: over dV with a 64 x 16 box (key-major)
     using L = Layout<HD, KEYMAJOR>;
-    static_assert(sizeof(Bars) <= L::kBarBytes, "barrier block");
+    static_assert(sizeof(Bars) <= L::kBarBytes && L::kR0 <= 3 && L::kR1 == 1, "barrier block");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
@@ -188,22 +231,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8 && lane == 0) {
         mbar_init(&bars->x_full, 1);
         mbar_init(&bars->x_empty, 1);
-        for (int s = 0; s < 2; ++s) {
-            // the TMA arrival, plus (key-major) the 32 producer lanes after writing lse2 / D
-            mbar_init(&bars->y_full[s], KEYMAJOR ? 33 : 1);
-            mbar_init(&bars->y_ok[s], 64);
-            mbar_init(&bars->y_empty[s], 1);
-            mbar_init(&bars->m2b_done[s], 1);
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(&bars->y0_full[s], 1);
+            mbar_init(&bars->y0_ok[s], 32);
+            mbar_init(&bars->y0_empty[s], 1);
+            mbar_init(&bars->vec_full[s], 32);
         }
+        mbar_init(&bars->y1_full, 1);
+        mbar_init(&bars->y1_ok, 32);
+        mbar_init(&bars->y1_empty, KEYMAJOR ? 2 : 1);  // dP's product through, and key-major dV's
+        for (int s = 0; s < 2; ++s) mbar_init(&bars->m2_done[s], 1);
         mbar_init(&bars->s_full, 1);
         mbar_init(&bars->dp_full, 1);
         mbar_init(&bars->a_done, 256);
         mbar_init(&bars->b_done, 256);
         mbar_init(&bars->dp_read, 256);
-        mbar_init(&bars->m2a_done, 1);
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->acc_empty, 256);
-        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->drain[0], 1);
+        mbar_init(&bars->drain[1], 1);
         bars->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -226,143 +272,157 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int walk_g = KEYMAJOR ? G : 1;
     if (warp >= 8) regs_decrease<kRegsOther>();
 
-    if (warp >= 10) {
-        // ------------------------------------------------------------ blank rows behind the document
-        const int at = threadIdx.x - 320;  // 0 .. 63
-        uint32_t n = 0;                    // fills so far (every step has its own)
-        bool ok = true;
-        ItemWalk wk;
-        for (wk.start(items, n_items, walk_g, H); ok && !wk.done(); wk.advance()) {
-            if (!wk.has()) continue;
-            const Tile o = decode_tile<KEYMAJOR>(wk.cur, p, G);
-            for (int s = 0; s < o.n_sub; ++s, ++n) {
-                const uint32_t st = n & 1;
-                ok = mbar_wait(&bars->y_full[st], (n >> 1) & 1, abort_flag, dev_status);
-                if (!ok) break;
-                int y_head, y_row;
-                step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
-                const int rows = o.doc_end - y_row;  // rows of the document
-                if (rows < kBlockN) {
-                    uint8_t* y = smem + L::kOffY + st * 2 * L::kTile;
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    // a row is 128 bytes of each 64-column chunk (the swizzle stays inside them)
-                    for (int x = at; x < (kBlockN - rows) * 8; x += 64)
-#pragma unroll
-                        for (int c = 0; c < 2 * HD / 64; ++c)
-                            *reinterpret_cast<uint4*>(y + c * L::kChunk + rows * 128 + x * 16) = z;
-                    fence_proxy_async_smem();
-                }
-                mbar_arrive(&bars->y_ok[st]);
-            }
-        }
-    } else if (warp == 8) {
+    if (warp == 10) {
         // ------------------------------------------------------------ producer
-        // X = (K, V) and Y = (Q, dO) (key-major), or the other way round
+        // Y = (Q, dO) (key-major) or (K, V), X the other two, by TMA. Y0 runs one step ahead of Y1: it is
+        // wanted first and has more buffers.
         const CUtensorMap* mx0 = KEYMAJOR ? &tm_k : &tm_q;
         const CUtensorMap* mx1 = KEYMAJOR ? &tm_v : &tm_do;
         const CUtensorMap* my0 = KEYMAJOR ? &tm_q : &tm_k;
         const CUtensorMap* my1 = KEYMAJOR ? &tm_do : &tm_v;
-        uint32_t oc = 0, n = 0;  // outer tiles and fills issued so far
+        Ring<L::kR0> y0;
+        uint32_t n0 = 0, n1 = 0, tiles_x = 0, tiles = 0;
         bool ok = true;
-        auto acquire = [&](uint64_t* bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
+        auto acquire = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
+            return ok;
         };
-        auto load_y = [&](const Tile& o, int s) -> bool {
-            const uint32_t st = n & 1;
-            if (!acquire(&bars->y_empty[st], ((n >> 1) & 1) ^ 1)) return false;
-            ++n;
-            int y_head, y_row;
-            step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
+        // the step whose Y1 (and X, if it is a tile's first) is still to come
+        bool lag = false, lag_first = false;
+        int lag_head = 0, lag_row = 0, lag_x_head = 0, lag_x_row = 0;
+        auto finish_lag = [&]() {
+            if (!lag) return;
+            if (lag_first) {
+                if (!acquire(&bars->x_empty, (tiles_x & 1) ^ 1)) return;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->x_full, 2 * L::kTile);
+                    for (int c = 0; c < HD / 64; ++c) {
+                        const int col = lag_x_head * HD + 64 * c;
+                        tma_load_2d(smem + L::kOffX + c * L::kChunk, mx0, col, lag_x_row, &bars->x_full);
+                        tma_load_2d(smem + L::kOffX + L::kTile + c * L::kChunk, mx1, col, lag_x_row, &bars->x_full);
+                    }
+                }
+                ++tiles_x;
+            }
+            if (!acquire(&bars->y1_empty, (n1 & 1) ^ 1)) return;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&bars->y_full[st], 2 * L::kTile);
-                uint8_t* y = smem + L::kOffY + st * 2 * L::kTile;
-                for (int c = 0; c < HD / 64; ++c) {
-                    tma_load_2d(y + c * L::kChunk, my0, y_head * HD + 64 * c, y_row, &bars->y_full[st]);
-                    tma_load_2d(y + L::kTile + c * L::kChunk, my1, y_head * HD + 64 * c, y_row, &bars->y_full[st]);
-                }
+                mbar_arrive_expect_tx(&bars->y1_full, L::kTile);
+                for (int c = 0; c < HD / 64; ++c)
+                    tma_load_2d(smem + L::kOffY1 + c * L::kChunk, my1, lag_head * HD + 64 * c, lag_row, &bars->y1_full);
             }
-            if (KEYMAJOR) {
-                // lse * log2(e) and D of the fill's queries (0 past the document end)
-                float* l2 = vec + st * 256;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = 4 * lane + e, qs = y_row + c;
-                    const bool in = qs < o.doc_end;
-                    const int64_t r = static_cast<int64_t>(qs) * H + y_head;
-                    l2[c] = in ? p.lse[r] * kLog2e : 0.f;
-                    l2[128 + c] = in ? dsum[r] : 0.f;
-                }
-                mbar_arrive(&bars->y_full[st]);
-            }
-            return true;
+            __syncwarp();
+            ++n1;
         };
         ItemWalk wk;
         for (wk.start(items, n_items, walk_g, H); ok && !wk.done(); wk.advance()) {
             if (!wk.has()) continue;
             const Tile o = decode_tile<KEYMAJOR>(wk.cur, p, G);
-            ok = load_y(o, 0);  // before X, whose buffer is free later
-            if (ok) ok = acquire(&bars->x_empty, (oc & 1) ^ 1);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars->x_full, 2 * L::kTile);
-                for (int c = 0; c < HD / 64; ++c) {
-                    tma_load_2d(smem + L::kOffX + c * L::kChunk, mx0, o.head * HD + 64 * c, o.row0, &bars->x_full);
-                    tma_load_2d(smem + L::kOffX + L::kTile + c * L::kChunk, mx1, o.head * HD + 64 * c, o.row0,
-                                &bars->x_full);
+            for (int s = 0; s < o.n_sub; ++s) {
+                if (!acquire(&bars->y0_empty[y0.i], y0.lap ^ 1)) break;
+                int y_head, y_row;
+                step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
+                if (lane == 0) {
+                    if (s == 0) bars->tile[tiles & 3] = TileRec{o.row0, o.head, o.doc_start, o.doc_end, o.piece};
+                    bars->step[y0.i] = StepRec{(s == 0 ? kFirst : 0) | (s + 1 == o.n_sub ? kLast : 0), y_row,
+                                               o.doc_end - y_row < kBlockN ? o.doc_end - y_row : kBlockN,
+                                               step_cols<KEYMAJOR>(o, s, p)};
+                    mbar_arrive_expect_tx(&bars->y0_full[y0.i], L::kTile);
+                    for (int c = 0; c < HD / 64; ++c)
+                        tma_load_2d(smem + L::kOffY0 + y0.i * L::kTile + c * L::kChunk, my0, y_head * HD + 64 * c, y_row,
+                                    &bars->y0_full[y0.i]);
                 }
+                if (KEYMAJOR) {
+                    // -lse * log2(e) and -D of the queries (0 past the document end), asynchronously too
+                    const uint32_t to = smem_u32(vec + y0.i * 256);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 32 * e + lane, qs = y_row + c;
+                        const bool inside = qs < o.doc_end;
+                        const int64_t r = inside ? static_cast<int64_t>(qs) * H + y_head : 0;
+                        cp_async_4_zfill(to + 4 * c, nlse + r, inside ? 4u : 0u);
+                        cp_async_4_zfill(to + 512 + 4 * c, nd + r, inside ? 4u : 0u);
+                    }
+                    cp_async_arrive(&bars->vec_full[y0.i]);
+                }
+                __syncwarp();
+                ++n0;
+                y0.next();
+                finish_lag();
+                lag = true;
+                lag_first = s == 0;
+                lag_head = y_head;
+                lag_row = y_row;
+                lag_x_head = o.head;
+                lag_x_row = o.row0;
             }
-            ++oc;
-            for (int s = 1; ok && s < o.n_sub; ++s) ok = load_y(o, s);
+            ++tiles;
         }
+        if (ok && acquire(&bars->y0_empty[y0.i], y0.lap ^ 1)) {
+            if (lane == 0) {
+                bars->step[y0.i].flags = kEnd;
+                mbar_arrive(&bars->y0_full[y0.i]);
+            }
+            __syncwarp();
+            finish_lag();
+        }
+        cp_async_wait_all();
         if (!ok && lane == 0) {
-            // Wait (bounded) for the copies this warp issued last into every buffer.
-            if (oc > 0) drain_wait(&bars->x_full, (oc - 1) & 1);
-            for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) drain_wait(&bars->y_full[i & 1], (i >> 1) & 1);
+            // Wait (bounded) for the copies issued last into every buffer.
+            if (tiles_x > 0) drain_wait(&bars->x_full, (tiles_x - 1) & 1);
+            if (n1 > 0) drain_wait(&bars->y1_full, (n1 - 1) & 1);
+            for (uint32_t i = n0 > 3 ? n0 - 3 : 0; i < n0; ++i) drain_wait(&bars->y0_full[i % 3], (i / 3) & 1);
         }
         __syncwarp();
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ blank rows behind the document
+        Ring<L::kR0> y0;
+        uint32_t n1 = 0;
+        int rows = kBlockN;       // of the step whose Y1 comes next
+        bool ok = true, lag = false;
+        auto blank = [&](int off, int from) {
+            if (from >= kBlockN) return;
+            uint8_t* y = smem + off + from * 128;
+            // a row is 128 bytes of each 64-column chunk (the swizzle stays inside them)
+            for (int x = lane; x < (kBlockN - from) * 8; x += 32)
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c)
+                    *reinterpret_cast<uint4*>(y + c * L::kChunk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+        };
+        for (;;) {  // (the producer's order)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->y0_full[y0.i], y0.lap, abort_flag, dev_status));
+            if (!ok) break;
+            const StepRec rec = bars->step[y0.i];
+            const bool end = (rec.flags & kEnd) != 0;
+            if (!end) blank(L::kOffY0 + y0.i * L::kTile, rec.rows);
+            mbar_arrive(&bars->y0_ok[y0.i]);
+            y0.next();
+            if (lag) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->y1_full, n1 & 1, abort_flag, dev_status));
+                if (!ok) break;
+                blank(L::kOffY1, rows);
+                mbar_arrive(&bars->y1_ok);
+                ++n1;
+            }
+            if (end) break;
+            rows = rec.rows;
+            lag = true;
+        }
     } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ the products S and dP
         if (lane == 0) {
-            constexpr uint32_t idesc1 = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
-            constexpr uint32_t idesc2 = idesc_bf16_f32(kBlockM, HD, 0, 1);
-            const uint32_t tm_s = tmem + L::kTmS, tm_dp = tmem + L::kTmDP;
-            const uint32_t x0 = sbase + L::kOffX, x1 = x0 + L::kTile;
-            uint32_t tiles = 0;   // outer tiles begun
+            constexpr uint32_t idesc = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 if (ok) ok = mbar_wait(bar, parity, abort_flag, dev_status);
             };
-            // The steps of all items in a row: where step g is, and the next one.
-            struct Step {
-                bool on, first, last;
-                int cols;
-            };
-            ItemWalk wk;
-            Tile o{};
-            int s = 0;
-            auto open = [&]() -> bool {  // the next item, if any
-                while (!wk.done() && !wk.has()) wk.advance();
-                if (wk.done()) return false;
-                o = decode_tile<KEYMAJOR>(wk.cur, p, G);
-                s = 0;
-                return true;
-            };
-            auto next = [&]() -> Step {
-                if (s == o.n_sub) {
-                    wk.advance();
-                    if (!open()) return Step{false, false, false, 0};
-                }
-                const Step x{true, s == 0, s + 1 == o.n_sub, step_cols<KEYMAJOR>(o, s, p)};
-                ++s;
-                return x;
-            };
-            // S or dP of step g: X (K-major) times Y (K-major), the first x.cols columns
-            auto product1 = [&](const Step& x, uint32_t g, uint32_t xt, int which, uint32_t d, uint64_t* full) {
+            // d = X_w times Y (both K-major), the first `cols` columns
+            auto product = [&](uint32_t d, int w, int y_off, int cols, uint64_t* full) {
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t id = (idesc1 & ~(0x3Fu << 17)) | (static_cast<uint32_t>(x.cols >> 3) << 17);
-                const uint64_t dx = desc_kmajor(xt, 0);
-                const uint64_t dy = desc_kmajor(sbase + L::kOffY + (g & 1) * 2 * L::kTile + which * L::kTile, 0);
+                const uint32_t id = KEYMAJOR ? idesc : (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(cols >> 3) << 17);
+                const uint64_t dx = desc_kmajor(sbase + L::kOffX + w * L::kTile, 0);
+                const uint64_t dy = desc_kmajor(sbase + y_off, 0);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {  // (as desc_kmajor steps)
                     const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
@@ -370,89 +430,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 umma_commit(full);
             };
-            // acc += A (TMEM, bf16 pairs; column half h at a + h * half) times Y's rows (MN-major)
-            auto product2 = [&](const Step& x, uint32_t g, uint32_t a, uint32_t half, int which, uint32_t acc,
-                                uint64_t* done) {
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t dy = desc_v(sbase + L::kOffY + (g & 1) * 2 * L::kTile + which * L::kTile, 0);
-#pragma unroll
-                for (int kk = 0; kk < kBlockN / 16; ++kk) {
-                    if (!KEYMAJOR && 16 * kk >= x.cols) continue;
-                    umma_f16_ts(acc, a + (kk >> 2) * half + (kk & 3) * 8, dy + kk * (2048 >> 4), idesc2,
-                                (!x.first || kk > 0) ? 1u : 0u);
-                }
-                umma_commit(done);
-            };
-            // the tile and fill of a step about to be multiplied
-            auto wait_inputs = [&](const Step& x, uint32_t g) {
-                if (x.first) {
+            Ring<L::kR0> y0;
+            uint32_t tiles = 0;
+            for (uint32_t g = 0; ok; ++g) {
+                wait(&bars->y0_ok[y0.i], y0.lap);
+                if (!ok) break;
+                const int flags = bars->step[y0.i].flags, cols = bars->step[y0.i].cols;
+                if (flags & kEnd) break;
+                if (flags & kFirst) {
                     wait(&bars->x_full, tiles & 1);
                     ++tiles;
                 }
-                wait(&bars->y_ok[g & 1], (g >> 1) & 1);
-            };
-            wk.start(items, n_items, walk_g, H);
-            uint32_t g = 0;
-            Step cur = open() ? next() : Step{false, false, false, 0};
-            if (cur.on) {
-                wait_inputs(cur, 0);
-                product1(cur, 0, x0, 0, tm_s, &bars->s_full);
-                product1(cur, 0, x1, 1, tm_dp, &bars->dp_full);
-                if (ok && cur.last) umma_commit(&bars->x_empty);
-            }
-            for (; ok && cur.on; ++g) {
-                const Step nxt = next();
-                // a new outer tile's X comes when this one's last products are through: they go first
-                const bool early = nxt.on && !nxt.first;
-                // stage A's end: key-major dV += P^T dO, then (its P being S's columns) the next S; query-
-                // major the next S at once
-                wait(&bars->a_done, g & 1);
-                if (KEYMAJOR) {
-                    if (cur.first && tiles > 1) wait(&bars->acc_empty, tiles & 1);
-                    product2(cur, g, tm_s, 64, 1, tmem + L::kTmAcc, &bars->m2a_done);
-                }
-                if (early) {
-                    wait_inputs(nxt, g + 1);
-                    if (KEYMAJOR) wait(&bars->m2a_done, g & 1);
-                    product1(nxt, g + 1, x0, 0, tm_s, &bars->s_full);
-                    if (!KEYMAJOR) {
-                        wait(&bars->dp_read, g & 1);
-                        product1(nxt, g + 1, x1, 1, tm_dp, &bars->dp_full);
-                        if (ok && nxt.last) umma_commit(&bars->x_empty);
-                    }
-                }
-                // stage B's end: dK += dS^T Q, or dQ += dS K
-                wait(&bars->b_done, g & 1);
-                if (KEYMAJOR) {
-                    product2(cur, g, tm_dp, 64, 0, tmem + L::kTmAcc + HD, &bars->m2b_done[0]);
-                } else {
-                    if (cur.first && tiles > 1) wait(&bars->acc_empty, tiles & 1);
-                    product2(cur, g, tmem + L::kTmDS + 64 * (g & 1), 32, 0, tmem + L::kTmAcc, &bars->m2b_done[g & 1]);
-                }
+                // S, when its columns are free: key-major P lay in them (dV's product), query-major once read
+                if (g > 0) wait(KEYMAJOR ? &bars->m2_done[0] : &bars->a_done, (g - 1) & 1);
+                product(tmem + L::kTmS, 0, L::kOffY0 + y0.i * L::kTile, cols, &bars->s_full);
+                // dP, likewise (dS lay in its columns)
+                wait(&bars->y1_ok, g & 1);
+                if (g > 0) wait(KEYMAJOR ? &bars->m2_done[1] : &bars->dp_read, (g - 1) & 1);
+                product(tmem + L::kTmDP, 1, L::kOffY1, cols, &bars->dp_full);
                 if (!ok) break;
-                umma_commit(&bars->y_empty[g & 1]);
-                if (cur.last) umma_commit(&bars->acc_full);
-                if (nxt.on && !early) {
-                    wait_inputs(nxt, g + 1);
-                    if (KEYMAJOR) wait(&bars->m2a_done, g & 1);
-                    product1(nxt, g + 1, x0, 0, tm_s, &bars->s_full);
-                    if (!KEYMAJOR) {
-                        wait(&bars->dp_read, g & 1);
-                        product1(nxt, g + 1, x1, 1, tm_dp, &bars->dp_full);
-                        if (ok && nxt.last) umma_commit(&bars->x_empty);
-                    }
-                }
-                if (KEYMAJOR && nxt.on) {  // dS lay in dP's columns
-                    wait(&bars->m2b_done[0], g & 1);
-                    product1(nxt, g + 1, x1, 1, tm_dp, &bars->dp_full);
-                    if (ok && nxt.last) umma_commit(&bars->x_empty);
-                }
-                cur = nxt;
+                umma_commit(&bars->y1_empty);
+                if (flags & kLast) umma_commit(&bars->x_empty);
+                y0.next();
             }
             // Wait (bounded) until every MMA this thread issued has finished.
-            umma_commit(&bars->drain);
-            drain_wait(&bars->drain, 0);
+            umma_commit(&bars->drain[0]);
+            drain_wait(&bars->drain[0], 0);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ the products dV and dK, or dQ
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kBlockM, HD, 0, 1);
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok) ok = mbar_wait(bar, parity, abort_flag, dev_status);
+            };
+            // acc (+)= A (TMEM, bf16 pairs; column half h at a + h * half) times Y's rows (MN-major)
+            auto product = [&](uint32_t acc, uint32_t a, uint32_t half, int y_off, bool first, int cols) {
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t dy = desc_v(sbase + y_off, 0);
+#pragma unroll
+                for (int kk = 0; kk < kBlockN / 16; ++kk) {
+                    if (!KEYMAJOR && 16 * kk >= cols) continue;
+                    umma_f16_ts(acc, a + (kk >> 2) * half + (kk & 3) * 8, dy + kk * (2048 >> 4), idesc,
+                                (!first || kk > 0) ? 1u : 0u);
+                }
+            };
+            Ring<L::kR0> y0;
+            uint32_t tiles = 0;
+            for (uint32_t g = 0; ok; ++g) {
+                wait(&bars->y0_ok[y0.i], y0.lap);
+                if (!ok) break;
+                const int flags = bars->step[y0.i].flags, cols = bars->step[y0.i].cols;
+                if (flags & kEnd) break;
+                const bool first = (flags & kFirst) != 0;
+                const int y0_off = L::kOffY0 + y0.i * L::kTile;
+                wait(KEYMAJOR ? &bars->a_done : &bars->b_done, g & 1);
+                if (first) {
+                    if (tiles > 0) wait(&bars->acc_empty, (tiles - 1) & 1);
+                    ++tiles;
+                }
+                if (KEYMAJOR) {
+                    product(tmem + L::kTmAcc, tmem + L::kTmS, 64, L::kOffY1, first, kBlockN);
+                    if (!ok) break;
+                    umma_commit(&bars->m2_done[0]);
+                    umma_commit(&bars->y1_empty);
+                    wait(&bars->b_done, g & 1);
+                    product(tmem + L::kTmAcc + HD, tmem + L::kTmDP, 64, y0_off, first, kBlockN);
+                    if (!ok) break;
+                    umma_commit(&bars->m2_done[1]);
+                } else {
+                    product(tmem + L::kTmAcc, tmem + L::kTmDS + 64 * (g & 1), 32, y0_off, first, cols);
+                    if (!ok) break;
+                    umma_commit(&bars->m2_done[g & 1]);
+                }
+                umma_commit(&bars->y0_empty[y0.i]);
+                if (flags & kLast) umma_commit(&bars->acc_full);
+                y0.next();
+            }
+            umma_commit(&bars->drain[1]);
+            drain_wait(&bars->drain[1], 0);
         }
         __syncwarp();
     } else {
@@ -462,31 +521,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = threadIdx.x & 127;  // TMEM lane == row of the outer tile
         const int r0 = (warp & 3) * 32;     // first row of this warp
         const uint32_t tm_lane = tmem + (static_cast<uint32_t>(r0) << 16);
-        const float scale_log2 = p.scale * kLog2e;
+        const uint64_t scale2 = f32x2(p.scale * kLog2e, p.scale * kLog2e);
         const int window = p.window;
-        uint32_t oc = 0, g = 0;  // outer tiles and steps done
+        uint32_t oc = 0, g = 0, tiles = 0;  // outer tiles and steps done, outer tiles begun
+        Ring<L::kR0> y0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
             return ok;
         };
-        ItemWalk wk;
-        for (wk.start(items, n_items, walk_g, H); ok && !wk.done(); wk.advance()) {
-            if (!wk.has()) continue;
-            const Tile o = decode_tile<KEYMAJOR>(wk.cur, p, G);
-            const int a = o.doc_start, b = o.doc_end;
-            const int slot = o.row0 + row;  // key slot (key-major) or query slot
-            const bool valid = slot < b;
-            float lse2 = 0.f, dd = 0.f;     // query-major: this row's lse * log2(e) and D
-            if (!KEYMAJOR && valid) {
-                const int64_t r = static_cast<int64_t>(slot) * H + o.head;
-                lse2 = p.lse[r] * kLog2e;
-                dd = dsum[r];
-            }
-            for (int s = 0; s < o.n_sub; ++s, ++g) {
+        TileRec o{};
+        uint64_t row_lse = 0, row_d = 0;  // query-major: this row's -lse * log2(e) and -D, twice
+        for (;; ++g) {
+            {
+                if (!wait(&bars->y0_full[y0.i], y0.lap)) break;  // (its record; the tile is long there)
+                const StepRec rec = bars->step[y0.i];
+                if (rec.flags & kEnd) break;
+                if (rec.flags & kFirst) {
+                    o = bars->tile[tiles & 3];
+                    ++tiles;
+                    const int slot = o.row0 + row;
+                    if (!KEYMAJOR && slot < o.doc_end) {
+                        const int64_t r = static_cast<int64_t>(slot) * H + o.head;
+                        const float l = nlse[r], d = nd[r];
+                        row_lse = f32x2(l, l);
+                        row_d = f32x2(d, d);
+                    }
+                }
+                const int a = o.doc_start, b = o.doc_end, y_row = rec.y_row, n_cols = rec.cols;
+                const int slot = o.row0 + row;  // key slot (key-major) or query slot
+                const bool valid = slot < b;
                 const uint32_t st = g & 1;
-                int y_head, y_row;
-                step_tile<KEYMAJOR>(o, s, G, y_head, y_row);
                 // visible columns of this row: [c_lo, c_hi], and those below c_sk
                 int c_lo, c_hi, c_sk = 0;
                 if (KEYMAJOR) {  // the queries that see key `slot`
@@ -500,12 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) c_hi = -1;
                 // What nobody reads is left out: columns behind the sinks' slices in a step over them alone,
                 // rows that are no sinks in a far piece (their sums are not kept).
-                const int n_cols = step_cols<KEYMAJOR>(o, s, p);
                 const bool idle = 64 * h >= n_cols || (KEYMAJOR && o.piece >= 0 && r0 >= p.sinks);
-                const float* l2v = vec + st * 256 + 64 * h;
+                const float* l2v = vec + y0.i * 256 + 64 * h;
                 // stage A: P of the half's 64 columns, kept for stage B in registers
                 float pr[64];
-                if (KEYMAJOR && !wait(&bars->y_full[st], (g >> 1) & 1)) break;  // lse2 / D
+                if (KEYMAJOR && !wait(&bars->vec_full[y0.i], y0.lap)) break;
                 if (!wait(&bars->s_full, g & 1)) break;
                 tc_fence_after();
                 if (!idle) {
@@ -519,21 +583,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();  // S may be overwritten from here on
                         mbar_arrive(&bars->a_done);
                     }
+                    // (pairs packed; the mask apart, so that tiles seen whole do not fetch its code)
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        ulonglong2 l4 = make_ulonglong2(row_lse, row_lse);
+                        if (KEYMAJOR) l4 = *reinterpret_cast<const ulonglong2*>(l2v + e);
+                        float x0, x1, x2, x3;
+                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), scale2, l4.x), x0, x1);
+                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), scale2, l4.y), x2, x3);
+                        pr[e] = ex2(x0);
+                        pr[e + 1] = ex2(x1);
+                        pr[e + 2] = ex2(x2);
+                        pr[e + 3] = ex2(x3);
+                    }
+                    uint32_t bits[2];  // bit e of bits[cc]: column 64 h + 32 cc + e is visible
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         const int cb = 64 * h + 32 * cc;
-                        const uint32_t bits = low_bits(c_hi + 1 - cb) & (~low_bits(c_lo - cb) | low_bits(c_sk - cb));
+                        bits[cc] = low_bits(c_hi + 1 - cb) & (~low_bits(c_lo - cb) | low_bits(c_sk - cb));
+                    }
+                    if (!__all_sync(0xffffffffu, (bits[0] & bits[1]) == ~0u)) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 l4 = make_float4(lse2, lse2, lse2, lse2);
-                            if (KEYMAJOR) l4 = *reinterpret_cast<const float4*>(l2v + 32 * cc + e);
-                            const float l2q[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float pe = ex2(fmaf(__uint_as_float(sv[32 * cc + e + x]), scale_log2, -l2q[x]));
-                                pr[32 * cc + e + x] = ((bits >> (e + x)) & 1u) ? pe : 0.f;
-                            }
-                        }
+                        for (int e = 0; e < 64; ++e) pr[e] = ((bits[e >> 5] >> (e & 31)) & 1u) ? pr[e] : 0.f;
                     }
                     if (KEYMAJOR) {
                         // P rounded to bf16 as the A operand of dV += P^T dO (stage B takes it unrounded)
@@ -566,15 +637,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t dk[32];
 #pragma unroll
                     for (int e = 0; e < 64; e += 4) {
-                        float4 d4 = make_float4(dd, dd, dd, dd);
-                        if (KEYMAJOR) d4 = *reinterpret_cast<const float4*>(l2v + 128 + e);
-                        dk[e >> 1] = pack_bf16x2(pr[e] * (__uint_as_float(dv[e]) - d4.x),
-                                                 pr[e + 1] * (__uint_as_float(dv[e + 1]) - d4.y));
-                        dk[(e >> 1) + 1] = pack_bf16x2(pr[e + 2] * (__uint_as_float(dv[e + 2]) - d4.z),
-                                                       pr[e + 3] * (__uint_as_float(dv[e + 3]) - d4.w));
+                        ulonglong2 d4 = make_ulonglong2(row_d, row_d);
+                        if (KEYMAJOR) d4 = *reinterpret_cast<const ulonglong2*>(l2v + 128 + e);
+                        float x0, x1, x2, x3;
+                        f32x2_split(mul_f32x2(f32x2(pr[e], pr[e + 1]),
+                                              add_f32x2(f32x2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), d4.x)), x0, x1);
+                        f32x2_split(mul_f32x2(f32x2(pr[e + 2], pr[e + 3]),
+                                              add_f32x2(f32x2(__uint_as_float(dv[e + 2]), __uint_as_float(dv[e + 3])), d4.y)), x2, x3);
+                        dk[e >> 1] = pack_bf16x2(x0, x1);
+                        dk[(e >> 1) + 1] = pack_bf16x2(x2, x3);
                     }
                     // query-major: the buffer's last product (two steps ago) must be through
-                    if (!KEYMAJOR && g >= 2 && !wait(&bars->m2b_done[st], ((g >> 1) & 1) ^ 1)) break;
+                    if (!KEYMAJOR && g >= 2 && !wait(&bars->m2_done[st], ((g >> 1) & 1) ^ 1)) break;
                     tmem_st32(KEYMAJOR ? tm_lane + L::kTmDP + 64 * h : tm_lane + L::kTmDS + 64 * st + 32 * h, dk);
                     tmem_wait_st();
                 } else if (!KEYMAJOR) {
@@ -582,12 +656,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 mbar_arrive(&bars->b_done);
+                y0.next();
+                if (!(rec.flags & kLast)) continue;
             }
-            if (!ok) break;
             // epilogue: accumulators -> bf16 rows of dQ, or of dK (scaled) and dV
             if (!wait(&bars->acc_full, oc & 1)) break;
             ++oc;
             tc_fence_after();
+            const int a = o.doc_start, b = o.doc_end, slot = o.row0 + row;
+            const bool valid = slot < b;
             const int out_heads = KEYMAJOR ? Hkv : H;
             const int64_t base = (static_cast<int64_t>(slot) * out_heads + o.head) * HD;
             bool store = true;  // rows of dQ, dK, dV in bf16
@@ -701,6 +778,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, L::kTmemCols);
 }
 
+// -D_i = -dO_i . O_i and -lse_i log2(e) of every row (slot, head): 8 lanes per row, 16-byte loads.
+template <int HD>
+__global__ void __launch_bounds__(256) attn_bwd_sinks_rows_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dout,
+                                                                  const float* __restrict__ lse, float* __restrict__ nlse,
+                                                                  float* __restrict__ nd, int64_t rows) {
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t r = gid >> 3;
+    const int r8 = static_cast<int>(gid & 7);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < rows) {
+        uint4 a[HD / 64], b[HD / 64];
+#pragma unroll
+        for (int t = 0; t < HD / 64; ++t) {
+            a[t] = __ldg(o + r * (HD / 8) + 8 * t + r8);
+            b[t] = __ldg(dout + r * (HD / 8) + 8 * t + r8);
+        }
+#pragma unroll
+        for (int t = 0; t < HD / 64; ++t) {
+            const uint32_t x[4] = {a[t].x, a[t].y, a[t].z, a[t].w}, y[4] = {b[t].x, b[t].y, b[t].z, b[t].w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                acc[w] = fmaf(__uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16),
+                              fmaf(__uint_as_float(x[w] & 0xFFFF0000u), __uint_as_float(y[w] & 0xFFFF0000u), acc[w]));
+        }
+    }
+    float d = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+    if (r < rows && r8 == 0) {
+        nd[r] = -d;
+        nlse[r] = -lse[r] * kLog2e;
+    }
+}
+
 // Block (document, kv head, 256 of the values): the sinks' rows of dk, dv of documents with far query
 // tiles, summed over the window's part and the pieces in order.
 __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProblem p, __nv_bfloat16* dk,
@@ -733,8 +844,8 @@ __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProble
 
 template <int HD, bool KEYMAJOR>
 cudaError_t launch_one(const AttnProblem& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                       const CUtensorMap& tdo, const CUtensorMap& tst, const CUtensorMap& tst2, const float* dsum,
-                       void* out_a, void* out_b, const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
+                       const CUtensorMap& tdo, const CUtensorMap& tst, const CUtensorMap& tst2, const float* nlse,
+                       const float* nd, void* out_a, void* out_b, const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
     using L = Layout<HD, KEYMAJOR>;
     int dev = 0, sms = 0;
     cudaError_t e;
@@ -744,33 +855,43 @@ cudaError_t launch_one(const AttnProblem& p, const CUtensorMap& tq, const CUtens
         (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     attn_bwd_sinks_kernel<HD, KEYMAJOR><<<sms, kThreads, L::kSmemBytes, stream>>>(
-        tq, tk, tv, tdo, tst, tst2, p, dsum, static_cast<__nv_bfloat16*>(out_a), static_cast<__nv_bfloat16*>(out_b),
+        tq, tk, tv, tdo, tst, tst2, p, nlse, nd, static_cast<__nv_bfloat16*>(out_a), static_cast<__nv_bfloat16*>(out_b),
         items, hdr);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+cudaError_t launch_attn_bwd_sinks_rows(const AttnProblem& p, const void* o, const void* dout, float* nlse, float* nd,
+                                       cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(p.total_tokens) * p.slot_mult * p.heads;
+    const unsigned blocks = static_cast<unsigned>((rows * 8 + 255) / 256);
+    const auto *a = static_cast<const uint4*>(o), *b = static_cast<const uint4*>(dout);
+    if (p.head_dim == 128) attn_bwd_sinks_rows_kernel<128><<<blocks, 256, 0, stream>>>(a, b, p.lse, nlse, nd, rows);
+    else attn_bwd_sinks_rows_kernel<64><<<blocks, 256, 0, stream>>>(a, b, p.lse, nlse, nd, rows);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                      const CUtensorMap& tm_v, const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
-                                     const float* dsum, void* dq, const int4* items, WorkspaceHeader* hdr,
+                                     const float* nlse, const float* nd, void* dq, const int4* items, WorkspaceHeader* hdr,
                                      cudaStream_t stream) {
     if (p.head_dim == 128)
-        return launch_one<128, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, dsum, dq, nullptr, items, hdr, stream);
+        return launch_one<128, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, nlse, nd, dq, nullptr, items, hdr, stream);
     if (p.head_dim == 64)
-        return launch_one<64, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, dsum, dq, nullptr, items, hdr, stream);
+        return launch_one<64, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, nlse, nd, dq, nullptr, items, hdr, stream);
     return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                        const CUtensorMap& tm_v, const CUtensorMap& tm_do, const CUtensorMap& tm_dk,
-                                       const CUtensorMap& tm_dv, const float* dsum, void* dk, void* dv,
+                                       const CUtensorMap& tm_dv, const float* nlse, const float* nd, void* dk, void* dv,
                                        const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
     cudaError_t e = cudaErrorInvalidValue;
     if (p.head_dim == 128)
-        e = launch_one<128, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, dsum, dk, dv, items, hdr, stream);
+        e = launch_one<128, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, nlse, nd, dk, dv, items, hdr, stream);
     else if (p.head_dim == 64)
-        e = launch_one<64, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, dsum, dk, dv, items, hdr, stream);
+        e = launch_one<64, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, nlse, nd, dk, dv, items, hdr, stream);
     if (e != cudaSuccess || p.sinks == 0) return e;
     attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads, (p.sinks * 2 * p.head_dim + 255) / 256), 256, 0, stream>>>(
         p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr);

@@ -179,20 +179,23 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
                                const float* dsum, void* dq, void* dk, void* dv, const int4* items,
                                WorkspaceHeader* hdr, int which, cudaStream_t stream);
 
-// Backward with window and sinks (bf16, head_dim 64 / 128; p.sinks, p.window may be 0): dQ over a
-// kSchedTilesQ list, dK / dV over a kSchedTilesK list (with far pieces, summed at the end). Maps as
-// launch_attn_bwd_tc.
+// Backward with window and sinks (bf16, head_dim 64 / 128; p.sinks, p.window may be 0): -lse log2(e) and
+// -D of every row into nlse, nd (float[slots][heads]); then dQ over a kSchedTilesQ list, dK / dV over a
+// kSchedTilesK list (with far pieces, summed at the end). Maps as launch_attn_bwd_tc.
+cudaError_t launch_attn_bwd_sinks_rows(const AttnProblem& p, const void* o, const void* dout,
+                                       float* nlse, float* nd, cudaStream_t stream);
 cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm_q,
                                      const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                      const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
-                                     const float* dsum, void* dq, const int4* items,
-                                     WorkspaceHeader* hdr, cudaStream_t stream);
+                                     const float* nlse, const float* nd, void* dq,
+                                     const int4* items, WorkspaceHeader* hdr,
+                                     cudaStream_t stream);
 cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& tm_q,
                                        const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                        const CUtensorMap& tm_do, const CUtensorMap& tm_dk,
-                                       const CUtensorMap& tm_dv, const float* dsum, void* dk,
-                                       void* dv, const int4* items, WorkspaceHeader* hdr,
-                                       cudaStream_t stream);
+                                       const CUtensorMap& tm_dv, const float* nlse,
+                                       const float* nd, void* dk, void* dv, const int4* items,
+                                       WorkspaceHeader* hdr, cudaStream_t stream);
 
 // RoPE preceded by the QK RMS-norm of every head row (weights may be NULL = ones).
 cudaError_t launch_qk_norm_rope(void* q, void* k, const float* q_weight, const float* k_weight,

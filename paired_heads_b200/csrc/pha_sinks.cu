@@ -58,11 +58,11 @@ FwdPlan fwd_plan(int batch, int max_len, int n_heads, int n_kv_heads, int head_d
 }
 
 // Backward: header, per-document scratch and work list of the query tiles, the same of the key tiles
-// (with far pieces; apart, so that a later call over the same documents keeps both lists), D, the far
-// pieces' partial sums.
+// (with far pieces; apart, so that a later call over the same documents keeps both lists), D (or -D),
+// -lse log2(e), the far pieces' partial sums.
 struct BwdPlan {
     int64_t items_q, items_k;
-    size_t list, keys, dsum, part, bytes;  // list: of a work list behind its header
+    size_t list, keys, dsum, nlse, part, bytes;  // list: of a work list behind its header
 };
 
 BwdPlan bwd_plan(int batch, int max_len, int total_tokens, int n_heads, int n_kv_heads, int head_dim,
@@ -79,7 +79,8 @@ BwdPlan bwd_plan(int batch, int max_len, int total_tokens, int n_heads, int n_kv
     w.list = kWorkspaceHeaderBytes + workspace_doc_bytes(batch);
     w.keys = padded(w.list + sizeof(int4) * static_cast<size_t>(w.items_q));
     w.dsum = w.keys + padded(w.list + sizeof(int4) * static_cast<size_t>(w.items_k));
-    w.part = w.dsum + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
+    w.nlse = w.dsum + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
+    w.part = w.nlse + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
     const int64_t slots = static_cast<int64_t>(total_tokens) * mult;
     w.bytes = w.part + (far ? padded(sizeof(float) * static_cast<size_t>(sink_part_slots(batch, slots, piece)) *
                                      (n_kv_heads / mult) * sinks * 2 * head_dim)
@@ -219,10 +220,12 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
     p.checked = hdr;
     const bool tc = dtype == PHA_BF16;
     // the scheduler also checks cu_seqlens; without a list to walk (CUDA cores) only that is used
-    if (build(kSchedTilesQ, 0, w.items_q) != cudaSuccess ||
-        launch_attn_bwd_dsum(p, o, dout, dsum, tc, stream) != cudaSuccess)
-        return PHA_ERR_CUDA;
-    if (!tc) return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, 0, stream));
+    if (build(kSchedTilesQ, 0, w.items_q) != cudaSuccess) return PHA_ERR_CUDA;
+    if (!tc) {
+        if (launch_attn_bwd_dsum(p, o, dout, dsum, 0, stream) != cudaSuccess) return PHA_ERR_CUDA;
+        return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, 0, stream));
+    }
+    float* nlse = reinterpret_cast<float*>(base + w.nlse);
     const uint64_t rows = static_cast<uint64_t>(total_tokens) * p.slot_mult;
     const uint64_t wq = static_cast<uint64_t>(p.heads) * head_dim, wk = static_cast<uint64_t>(p.kv_heads) * head_dim;
     CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
@@ -232,10 +235,12 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
         !encode_slot_map(&tdv, dv, wk, rows, 16))
         return PHA_ERR_CUDA;
     if (launch_attn_bwd_zero_outside(p, dq, dk, dv, stream) != cudaSuccess ||
-        launch_attn_bwd_sinks_dq(p, tq, tk, tv, tdo, tdq, dsum, dq, list(0), hdr, stream) != cudaSuccess ||
+        launch_attn_bwd_sinks_rows(p, o, dout, nlse, dsum, stream) != cudaSuccess ||
+        launch_attn_bwd_sinks_dq(p, tq, tk, tv, tdo, tdq, nlse, dsum, dq, list(0), hdr, stream) != cudaSuccess ||
         build(kSchedTilesK, w.keys, w.items_k) != cudaSuccess)
         return PHA_ERR_CUDA;
-    return of(launch_attn_bwd_sinks_dkdv(p, tq, tk, tv, tdo, tdk, tdv, dsum, dk, dv, list(w.keys), hdr_k, stream));
+    return of(launch_attn_bwd_sinks_dkdv(p, tq, tk, tv, tdo, tdk, tdv, nlse, dsum, dk, dv, list(w.keys), hdr_k,
+                                         stream));
 }
 
 }  // extern "C"

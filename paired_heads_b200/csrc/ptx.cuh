@@ -110,6 +110,11 @@ __device__ __forceinline__ void cp_async_16_zfill(uint32_t smem_dst, const void*
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes)
                  : "memory");
 }
+// 4 bytes (through L1), zeros for bytes = 0.
+__device__ __forceinline__ void cp_async_4_zfill(uint32_t smem_dst, const void* gsrc, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes)
+                 : "memory");
+}
 // Arrive once on `bar` when every cp.async this thread has issued so far has landed (the barrier's count
 // includes the arrival). Readers through the async proxy still need a proxy fence after the wait.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
