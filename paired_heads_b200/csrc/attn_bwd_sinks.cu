@@ -23,7 +23,7 @@
 // are computed; while the next stage A runs, dK += dS^T Q and the next dP. (Both stages after both
 // products, as in attn_bwd_tc.cu: 798 us for dK / dV of 2 x 8192 tokens, 32 / 8 heads of 128, window
 // 1024, 675 for dQ; the two column halves of a step staggered instead: 680 and 574, the halves' N = 64
-// products reading X twice; this one: 603 and 441, 4,200 and 3,000 clocks a step.) What is left over the
+// products reading X twice; this one: 637 and 441, 4,400 and 3,000 clocks a step.) What is left over the
 // products' 2,050 and 1,540 clocks is the chain S -> P -> dV -> next S, P lying in S's columns: with 256
 // columns of accumulators TMEM has no room for a second S.
 // TMEM columns: S [0, 128), dP [128, 256), accumulators from 256 (dV, dK or dQ). Key-major, P^T and dS^T
@@ -86,7 +86,7 @@ struct Layout {
 // y0_full or y0_ok), and of each outer tile (four of them: a step three before a tile's first one belongs
 // at the latest to the tile three before it, so everybody has left the one four before). The other roles
 // decode nothing: their code has to stay small beside the elementwise loops, whose instructions it pushes
-// out of the cache (each role walking the list by itself: 656 us instead of 603 for dK / dV, 496 instead
+// out of the cache (each role walking the list by itself: 656 us instead of 637 for dK / dV, 496 instead
 // of 441 for dQ, 2 x 8192 tokens, 32 / 8 heads of 128, window 1024).
 struct StepRec {
     int flags;  // kFirst, kLast step of its outer tile; kEnd: no step, the list is done
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++tiles;
                 }
                 if (KEYMAJOR) {
+                    wait(&bars->y1_ok, g & 1);  // (P needs S alone: dO may still be on its way)
                     product(tmem + L::kTmAcc, tmem + L::kTmS, 64, L::kOffY1, first, kBlockN);
                     if (!ok) break;
                     umma_commit(&bars->m2_done[0]);

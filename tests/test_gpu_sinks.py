@@ -135,6 +135,27 @@ def test_forward_and_backward(pha, case):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("H,Hkv,hd,window,paired", [(6, 6, 128, 128, True), (16, 4, 128, 300, False),
+                                                    (6, 3, 64, 128, False)])
+def test_a_busy_device_gives_the_bits_of_a_document_alone(pha, H, Hkv, hd, window, paired):
+    """Loads of a full device come late and in any order; a document's gradients do not depend on what
+    else is computed beside it (its tiles, pieces and sums are its own)."""
+    lens = [1479, 700, 2047, 130, 1, 1024] * 6
+    c = Case(lens, H, Hkv, hd, BF16, window, 8, paired, seed=3)
+    o, lse = c.forward(pha)
+    grads = c.backward(pha, o, lse)
+    for _ in range(3):
+        for a, b in zip(grads, c.backward(pha, o, lse)):
+            assert torch.equal(a, b)
+    cu = c.cu.tolist()
+    for i in (0, 2, 3, 20, 35):
+        lo, hi = cu[i], cu[i + 1]
+        one = Case([hi - lo], H, Hkv, hd, BF16, window, 8, paired, max_len=c.max_len)
+        one.q, one.k, one.v, one.dout = (x[lo:hi].clone() for x in (c.q, c.k, c.v, c.dout))
+        for a, b in zip(grads, one.backward(pha, o[lo:hi].clone(), lse[lo:hi].clone())):
+            assert torch.equal(a[lo:hi], b)
+
+
 @pytest.mark.parametrize("dtype,hd", [(BF16, 64), (BF16, 128), (F32, 32)])
 def test_rows_outside_the_documents(pha, dtype, hd):
     c = Case((150, 290), 4, 2, hd, dtype, 40, 6, False, head=3, tail=70, max_len=1000, scale=0.3)
