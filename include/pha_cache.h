@@ -59,10 +59,12 @@ size_t pha_attn_paged_workspace_bytes(int batch, int max_q, int max_kv, int tota
  *   the second product); f32 with head_dim 1 .. 128 (CUDA cores).
  *   Rows of q behind cu_seqlens[batch] are not touched. A sequence whose lengths are out of range
  *   (kv_lens < new tokens, beyond max_kv or max_pages * page_size, more than max_q new tokens, rows
- *   outside q) raises status 1 and its rows are not written, nor any row if cu_seqlens decreases.
+ *   outside q) raises status 1 and its rows are not written; if cu_seqlens decreases anywhere, which
+ *   rows are written is unspecified.
  *   A needed entry that is no page raises status 4; the rows that see it are then unspecified.
  *   Errors: PHA_ERR_INVALID (NULL or misaligned pointers, sizes, head counts as in pha_attn_fwd,
- *   page_size no power of two, n_pages * page_size * n_kv_heads beyond 2^31 - 1 rows, sinks < 0),
+ *   page_size no power of two, n_pages * page_size * n_kv_heads or total_q * n_heads beyond
+ *   2^31 - 1 rows, sinks < 0),
  *   PHA_ERR_UNSUPPORTED (type / head_dim), PHA_ERR_WORKSPACE.
  */
 pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages,
@@ -110,8 +112,8 @@ pha_status pha_cache_fork(int32_t* page_table, int max_pages, int32_t* kv_lens, 
  *   the call) gets a page of its own with the shared one's contents, in all layers, first.
  *   page_bytes: bytes of one page of one layer and of K or V alone (page_size * n_kv_heads * head_dim
  *   * element size), a multiple of 16.
- *   Too few free pages: status 5; out of range, or longer than max_pages pages: status 1; a last page
- *   that is none: status 4. Nothing is changed then. Count: pages taken.
+ *   Too few free pages: status 5; out of range, or longer than max_pages pages or 2^31 - 1 tokens:
+ *   status 1; a last page that is none: status 4. Nothing is changed then. Count: pages taken.
  */
 pha_status pha_cache_reserve(int32_t* page_table, int max_pages, int32_t* kv_lens, int n_seqs,
                              int32_t* page_refs, int n_pages, int page_size, const int32_t* seqs,

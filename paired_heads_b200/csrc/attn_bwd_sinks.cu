@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap tm_st, const __grid_constant__ CUtensorMap tm_st2,
                           const AttnProblem p, const float* __restrict__ nlse, const float* __restrict__ nd,
                           __nv_bfloat16* __restrict__ out_a,
-                          __nv_bfloat16* __restrict__ out_b, const int4* __restrict__ items, WorkspaceHeader* hdr) {
+                          __nv_bfloat16* __restrict__ out_b, const int4* __restrict__ items,
+                          const WorkspaceHeader* hdr, int* dev_status) {
     // out_a: dQ (query-major) or dK (key-major); out_b: dV (key-major); tm_st: a map over dQ with a 64 x
     // 32 box or over dK with a 64 x 16 box; tm_st2: over dV with a 64 x 16 box (key-major)
     using L = Layout<HD, KEYMAJOR>;
@@ -223,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
     float* vec = reinterpret_cast<float*>(smem + L::kOffVec);
     volatile int* abort_flag = &bars->abort;
-    int* dev_status = &hdr->status;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
 
-    const int n_items = *reinterpret_cast<volatile int*>(&hdr->n_items);
+    const int n_items = *reinterpret_cast<const volatile int*>(&hdr->n_items);
     const int H = p.heads, Hkv = p.kv_heads, G = H / Hkv;
     // key-major: one item per kv head (that of the group's first query head)
     const int walk_g = KEYMAJOR ? G : 1;
@@ -846,7 +846,8 @@ __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProble
 template <int HD, bool KEYMAJOR>
 cudaError_t launch_one(const AttnProblem& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tdo, const CUtensorMap& tst, const CUtensorMap& tst2, const float* nlse,
-                       const float* nd, void* out_a, void* out_b, const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
+                       const float* nd, void* out_a, void* out_b, const int4* items, const WorkspaceHeader* hdr,
+                       int* status, cudaStream_t stream) {
     using L = Layout<HD, KEYMAJOR>;
     int dev = 0, sms = 0;
     cudaError_t e;
@@ -857,7 +858,7 @@ cudaError_t launch_one(const AttnProblem& p, const CUtensorMap& tq, const CUtens
         return e;
     attn_bwd_sinks_kernel<HD, KEYMAJOR><<<sms, kThreads, L::kSmemBytes, stream>>>(
         tq, tk, tv, tdo, tst, tst2, p, nlse, nd, static_cast<__nv_bfloat16*>(out_a), static_cast<__nv_bfloat16*>(out_b),
-        items, hdr);
+        items, hdr, status);
     return cudaGetLastError();
 }
 
@@ -875,24 +876,29 @@ cudaError_t launch_attn_bwd_sinks_rows(const AttnProblem& p, const void* o, cons
 
 cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                      const CUtensorMap& tm_v, const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
-                                     const float* nlse, const float* nd, void* dq, const int4* items, WorkspaceHeader* hdr,
-                                     cudaStream_t stream) {
+                                     const float* nlse, const float* nd, void* dq, const int4* items,
+                                     const WorkspaceHeader* hdr, int* status, cudaStream_t stream) {
     if (p.head_dim == 128)
-        return launch_one<128, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, nlse, nd, dq, nullptr, items, hdr, stream);
+        return launch_one<128, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, nlse, nd, dq, nullptr, items, hdr, status,
+                                 stream);
     if (p.head_dim == 64)
-        return launch_one<64, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, nlse, nd, dq, nullptr, items, hdr, stream);
+        return launch_one<64, false>(p, tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dq, nlse, nd, dq, nullptr, items, hdr, status,
+                                 stream);
     return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                        const CUtensorMap& tm_v, const CUtensorMap& tm_do, const CUtensorMap& tm_dk,
                                        const CUtensorMap& tm_dv, const float* nlse, const float* nd, void* dk, void* dv,
-                                       const int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
+                                       const int4* items, const WorkspaceHeader* hdr, int* status,
+                                       cudaStream_t stream) {
     cudaError_t e = cudaErrorInvalidValue;
     if (p.head_dim == 128)
-        e = launch_one<128, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, nlse, nd, dk, dv, items, hdr, stream);
+        e = launch_one<128, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, nlse, nd, dk, dv, items, hdr, status,
+                              stream);
     else if (p.head_dim == 64)
-        e = launch_one<64, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, nlse, nd, dk, dv, items, hdr, stream);
+        e = launch_one<64, true>(p, tm_q, tm_k, tm_v, tm_do, tm_dk, tm_dv, nlse, nd, dk, dv, items, hdr, status,
+                              stream);
     if (e != cudaSuccess || p.sinks == 0) return e;
     attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads, (p.sinks * 2 * p.head_dim + 255) / 256), 256, 0, stream>>>(
         p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr);

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_decode_kernel(const GatherPr
         for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            if (part_m[i][row] == -INFINITY) continue;  // nothing visible in this warp's steps
+            if (part_l[i][row] == 0.f) continue;  // nothing visible in this warp's steps
             const float w = ex2(part_m[i][row] - top);
             sum = fmaf(w, part_l[i][row], sum);
             const float* from = reinterpret_cast<const float*>(smem + i * kStages * stage_bytes<HD>()) + row * HD;
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_decode_kernel(const GatherPr
             float* dst = p.part_o + (split * all_rows + out) * HD;
 #pragma unroll
             for (int e = 0; e < HD / 32; ++e) dst[32 * e + lane] = acc[e] * inv;
-            if (lane == 0) p.part_lse[split * all_rows + out] = sum > 0.f ? top + log2f(sum) : -INFINITY;
+            if (lane == 0) p.part_lse[split * all_rows + out] = sum != 0.f ? top + log2f(sum) : -INFINITY;  // (NaN stays)
         }
     }
 }

@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 make_float4(__uint_as_float(ov[e]) * inv_l, __uint_as_float(ov[e + 1]) * inv_l,
                                             __uint_as_float(ov[e + 2]) * inv_l, __uint_as_float(ov[e + 3]) * inv_l);
                 }
-                if (valid) p.part_lse[part_row] = l > 0.f ? m + log2f(l) : -INFINITY;
+                if (valid) p.part_lse[part_row] = l != 0.f ? m + log2f(l) : -INFINITY;  // (NaN stays)
             } else {
                 const int out_row = tok * H + chunk * p.pack + (kBlockM * r + row - tok * p.pack);  // from q0's
                 // O -> bf16 through this sub-tile's Q slot (its last S has completed): each warp stages

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(GatherProblem
 #pragma unroll
         for (int t = 0; t < kMaxDim / 32; ++t)
             if (lane + 32 * t < D) o[lane + 32 * t] = acc[t] * inv;
-        if (lane == 0) p.part_lse[split * rows + row] = l > 0.f ? m + log2f(l) : -INFINITY;
+        if (lane == 0) p.part_lse[split * rows + row] = l != 0.f ? m + log2f(l) : -INFINITY;  // (NaN stays)
     }
 }
 

@@ -195,37 +195,37 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(CacheArgs c, const in
                                                            int page_shift) {
     __shared__ int shared_code;
     __shared__ int sums[kThreads / 32];
+    __shared__ int64_t needs[kThreads / 32];
     grid_dep_launch();  // the copy kernel may come up; it waits for this one's end
     const int page_size = 1 << page_shift;
     int code = check_list(c, seqs, nullptr, n, &shared_code);
     // what each sequence needs: its own copy of a shared last page, then pages for the rest
-    int total = 0;
+    int64_t total = 0;
     if (code == DEV_OK) {
         for (int base = 0; base < n; base += kThreads) {
             const int i = base + threadIdx.x;
-            int need = 0;
+            int64_t need = 0;
             if (i < n) {
                 const int s = seqs[i];
                 const int64_t len = c.lens[s], grow = new_tokens[i];
                 const int64_t have = (len + page_size - 1) >> page_shift;
                 const int64_t want = (len + grow + page_size - 1) >> page_shift;
                 int shared_page = -1;
-                if (len < 0 || grow < 0 || want > c.max_pages) {
+                if (len < 0 || grow < 0 || len + grow > INT32_MAX || want > c.max_pages) {
                     code = DEV_BAD_SEQLENS;
                 } else if (grow > 0 && (len & (page_size - 1)) != 0) {
                     const int last = c.table[static_cast<int64_t>(s) * c.max_pages + have - 1];
                     if (last < 0 || last >= c.n_pages) code = DEV_BAD_PAGE;
                     else if (c.refs[last] > 1) shared_page = last;
                 }
-                if (code == DEV_OK) need = static_cast<int>(want - have) + (shared_page >= 0 ? 1 : 0);
+                if (code == DEV_OK) need = want - have + (shared_page >= 0 ? 1 : 0);
                 c.copy_src[i] = shared_page;
-                c.need[i] = need;
+                c.need[i] = static_cast<int>(need);
             }
-            int chunk;
-            const int before = cta_exclusive_scan<kThreads>(need, sums, chunk);
-            if (i < n) c.first[i] = total + before;
-            // a total beyond the pool fails below; stop adding before it can overflow
-            total = total > c.n_pages ? total : total + chunk;
+            int64_t chunk;
+            const int64_t before = cta_exclusive_scan<kThreads>(need, needs, chunk);
+            if (i < n) c.first[i] = static_cast<int>(total + before);  // (read only if the pool has them all)
+            total += chunk;
         }
         code = cta_code(code, &shared_code);
     }
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(CacheArgs c, const in
     if (code == DEV_OK && total > 0) {
         int found = 0;
         if (total <= c.n_pages)
-            found = scan_pages(c.refs, 0, c.n_pages, 0, total, sums,
+            found = scan_pages(c.refs, 0, c.n_pages, 0, static_cast<int>(total), sums,
                                [](int r) { return r == 0; }, [&](int rank, int page) { c.pages[rank] = page; });
         if (found < total) code = DEV_NO_PAGES;
         __syncthreads();  // the list is read by other threads next
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(CacheArgs c, const in
         }
     }
     if (threadIdx.x == 0) c.hdr->n_copies = n;
-    finish(c, DEV_OK, total);
+    finish(c, DEV_OK, static_cast<int>(total));
 }
 
 // -------------------------------------------------------------------------------------- compact

@@ -188,14 +188,15 @@ cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm
                                      const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                      const CUtensorMap& tm_do, const CUtensorMap& tm_dq,
                                      const float* nlse, const float* nd, void* dq,
-                                     const int4* items, WorkspaceHeader* hdr,
-                                     cudaStream_t stream);
+                                     const int4* items, const WorkspaceHeader* hdr,
+                                     int* status, cudaStream_t stream);
 cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& tm_q,
                                        const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                        const CUtensorMap& tm_do, const CUtensorMap& tm_dk,
                                        const CUtensorMap& tm_dv, const float* nlse,
                                        const float* nd, void* dk, void* dv, const int4* items,
-                                       WorkspaceHeader* hdr, cudaStream_t stream);
+                                       const WorkspaceHeader* hdr, int* status,
+                                       cudaStream_t stream);
 
 // RoPE preceded by the QK RMS-norm of every head row (weights may be NULL = ones).
 cudaError_t launch_qk_norm_rope(void* q, void* k, const float* q_weight, const float* k_weight,

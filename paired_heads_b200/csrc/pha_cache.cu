@@ -218,6 +218,7 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
                 int page_size = 0) {
     if (batch <= 0 || max_q < 0 || max_kv < 0 || total_q < 0 || total_q > (1 << 28) ||
         max_kv > (1 << 29) || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
+        static_cast<int64_t>(total_q) * n_heads > INT32_MAX ||
         n_heads % n_kv_heads != 0 || head_dim <= 0 || head_dim > 128 || sinks < 0 ||
         (paired != 0 && paired != 1) || (paired && ((n_heads & 1) || (n_kv_heads & 1))))
         return false;
@@ -255,7 +256,9 @@ bool paged_plan(PagedPlan& w, int batch, int max_q, int max_kv, int total_q, int
         w.bytes = w.space.bytes;
         return true;
     }
+    // (no more splits than a grid's second dimension)
     w.split_keys = kRowsSplitKeys;
+    while ((most + w.split_keys - 1) / w.split_keys > 65535) w.split_keys *= 2;
     if (w.decode) {
         // One wave of blocks where the (sequence, kv head) pairs leave room for several ranges each; ranges
         // of at most kDecodeMaxSplit keys where they do not, so that long histories do not outlast the

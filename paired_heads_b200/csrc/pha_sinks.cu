@@ -22,6 +22,7 @@ pha_status shape_status(int batch, int max_len, int total_tokens, int n_heads, i
                         int head_dim, pha_dtype dtype, int sinks, int paired, float scale) {
     if ((dtype != PHA_BF16 && dtype != PHA_F32) || batch <= 0 || max_len < 0 || total_tokens < 0 ||
         total_tokens > (1 << 29) || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
+        static_cast<int64_t>(total_tokens) * n_heads > INT32_MAX ||
         n_heads % n_kv_heads != 0 || head_dim <= 0 || sinks < 0 || (paired != 0 && paired != 1) ||
         !(scale == scale) || (paired && ((n_heads & 1) || (n_kv_heads & 1))))
         return PHA_ERR_INVALID;
@@ -236,11 +237,12 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
         return PHA_ERR_CUDA;
     if (launch_attn_bwd_zero_outside(p, dq, dk, dv, stream) != cudaSuccess ||
         launch_attn_bwd_sinks_rows(p, o, dout, nlse, dsum, stream) != cudaSuccess ||
-        launch_attn_bwd_sinks_dq(p, tq, tk, tv, tdo, tdq, nlse, dsum, dq, list(0), hdr, stream) != cudaSuccess ||
+        launch_attn_bwd_sinks_dq(p, tq, tk, tv, tdo, tdq, nlse, dsum, dq, list(0), hdr, &hdr->status,
+                                 stream) != cudaSuccess ||
         build(kSchedTilesK, w.keys, w.items_k) != cudaSuccess)
         return PHA_ERR_CUDA;
     return of(launch_attn_bwd_sinks_dkdv(p, tq, tk, tv, tdo, tdk, tdv, nlse, dsum, dk, dv, list(w.keys), hdr_k,
-                                         stream));
+                                         &hdr->status, stream));  // (one status word for the call)
 }
 
 }  // extern "C"

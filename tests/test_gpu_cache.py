@@ -323,3 +323,31 @@ def test_page_calls_in_a_graph(pha):
         c.plain.reserve([2, 3, 4], [1, 9, 2])
         c.plain.free([2, 3, 4])
         c.same()
+
+
+def test_reserving_more_than_31_bits_of_pages(pha):
+    """The pages asked for add up past 2^31: refused as too many, nothing changed."""
+    n_seqs, max_pages = 4, 1 << 29
+    table = torch.empty(n_seqs, max_pages, dtype=torch.int32, device="cuda")
+    lens, refs = i32([0] * n_seqs), i32([0] * 8)
+    pool = [torch.zeros(1, 8, 1, 1, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ws = torch.empty(pha.pha_cache_workspace_bytes(8, n_seqs), dtype=torch.uint8, device="cuda")
+    status = i32([0])
+    pha.pha_cache_reserve(table, lens, refs, i32(range(4)), i32([max_pages] * 4), *pool, ws, status=status)
+    assert status.item() == 5 and not lens.any() and not refs.any()
+    assert pha.pha_attn_status(ws) == (5, 0)
+
+
+def test_reserving_past_31_bits_of_tokens(pha):
+    page, max_pages = 1 << 20, 1 << 12
+    table = torch.full((1, max_pages), -1, dtype=torch.int32, device="cuda")
+    have = (1 << 31) - 10
+    table[0, (have - 1) // page] = 1
+    lens, refs = i32([have]), i32([0, 1, 0])
+    pool = [torch.zeros(1, 3, page, 1, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ws = torch.empty(pha.pha_cache_workspace_bytes(3, 1), dtype=torch.uint8, device="cuda")
+    for new, code in ((9, 0), (1, 1)):
+        status = i32([0])
+        pha.pha_cache_reserve(table, lens, refs, i32([0]), i32([new]), *pool, ws, status=status)
+        assert status.item() == code and lens.item() == (1 << 31) - 1
+        assert refs.tolist() == [0, 1, 0]

@@ -183,6 +183,79 @@ def test_bad_pages_are_reported(pha, q, entry):
     assert (np.abs(got - want) <= ref.bo.reshape(o.shape)[a:z]).all()
 
 
+@pytest.mark.parametrize("q,kv,heads,dtype", [
+    ((1, 1), (300, 5000), (8, 2), BF16),     # decoding: one range, and several
+    ((3, 1), (40, 2000), (4, 4), BF16),
+    ((90, 40), (300, 9000), (8, 2), BF16),   # chunks, some of them cut between shares
+    ((2, 3), (90, 3000), (4, 2), F32),
+])
+def test_a_nan_query_stays_in_its_row(pha, q, kv, heads, dtype):
+    c = Case(q, kv, *heads, 64, dtype, 16)
+    rows = [0, c.q.shape[0] - 1]
+    c.q[rows[0], 1] = float("nan")
+    c.q[rows[1], 2, 3] = float("nan")
+    o, lse = c.run(pha)
+    assert torch.isnan(o[rows[0], 1]).all() and torch.isnan(lse[rows[0], 1])
+    assert torch.isnan(o[rows[1], 2]).all() and torch.isnan(lse[rows[1], 2])
+    assert torch.isnan(o).sum().item() == 2 * 64 and torch.isnan(lse).sum().item() == 2
+    for x, h in ((rows[0], 1), (rows[1], 2)):
+        c.q[x, h] = 0
+    ref = c.reference()
+    good, good_lse = c.run(pha)
+    ref.check(good, good_lse)
+    for x, h in ((rows[0], 1), (rows[1], 2)):
+        o[x, h], lse[x, h] = good[x, h], good_lse[x, h]
+    ref.check(o, lse)
+
+
+def test_one_workspace_for_every_kind_of_step(pha):
+    """Decoding, chunks and their captured forms take turns on one workspace of the largest size."""
+    cases = [Case((1,) * 5, (900, 20, 4000, 1, 77), 8, 2, 64, BF16, 16, seed=1),
+             Case((90, 3, 200), (2000, 700, 200), 8, 2, 128, BF16, 32, seed=2),
+             Case((2, 2), (3000, 100), 6, 6, 128, BF16, 16, window=100, sinks=4, paired=True, seed=3),
+             Case((50, 1, 0, 64), (400, 900, 3, 64), 4, 4, 64, BF16, 64, window=64, sinks=9, seed=4),
+             Case((5, 1), (900, 2500), 4, 2, 32, F32, 16, seed=5)]
+    refs = [c.reference() for c in cases]
+    ws = max((c.workspace(pha) for c in cases), key=lambda w: w.numel())
+    outs = [(torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")) for c in cases]
+    graphs = []
+    for c, (o, lse) in zip(cases, outs):
+        c.call(pha, o, lse, ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call(pha, o, lse, ws)
+        graphs.append(g)
+    for turn in range(3):
+        for i in (0, 1, 2, 3, 4, 3, 1, 0, 4, 2):
+            o, lse = outs[i]
+            o.fill_(float("nan"))
+            lse.fill_(float("nan"))
+            if (turn + i) % 2:
+                graphs[i].replay()
+            else:
+                cases[i].call(pha, o, lse, ws)
+            refs[i].check(o, lse)
+    assert all(c.status.item() == 0 for c in cases)
+
+
+def test_a_long_float32_cache_with_many_ranges(pha):
+    """Ranges of keys past 65,535 get longer instead of more."""
+    n = 65535 * 1024 + 5000
+    k = torch.zeros(n // 256 + 1, 256, 1, 1, device="cuda")
+    v = torch.ones_like(k)
+    table = torch.arange(k.shape[0], dtype=torch.int32, device="cuda")[None]
+    q = torch.ones(1, 1, 1, device="cuda")
+    k.view(-1)[n - 3] = 30.0                   # e^30 against n terms of e^0
+    v.view(-1)[n - 3] = 3.0
+    o, lse = torch.empty_like(q), torch.empty(1, 1, device="cuda")
+    one = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pha.pha_attn_paged_workspace_bytes(1, 1, n, 1, 1, 1, 1, F32), dtype=torch.uint8, device="cuda")
+    pha.pha_attn_paged_fwd(q, k, v, table, one(0, 1), one(n), 1, n, o, lse, ws, scale=1.0)
+    e = np.exp(30.0)
+    assert abs(o.item() - (3 * e + n - 1) / (e + n - 1)) < 1e-5
+    assert abs(lse.item() - np.log(e + n - 1)) < 1e-4
+
+
 def test_decode_graph_follows_growing_lengths(pha):
     """One captured step serves lengths that grow on the device, up to max_kv."""
     c = Case((1, 1, 1), (400, 37, 260), 8, 2, 64, BF16, 16, max_kv=500)

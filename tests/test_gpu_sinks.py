@@ -281,3 +281,41 @@ def test_training_step_in_a_graph(pha):
     g.replay()
     for a, b in zip((o, lse, *eager), out):
         assert torch.equal(a, b)
+
+
+def test_one_workspace_for_every_shape(pha):
+    """Different problems take turns on one forward and one backward workspace, eagerly and captured."""
+    cases = [Case((700, 129, 1), 8, 2, 128, BF16, 100, 4, False, seed=1),
+             Case((300, 5, 190), 6, 6, 128, BF16, 128, 8, True, seed=2),
+             Case((1500,), 2, 2, 64, BF16, 60, 4, False, seed=3),
+             Case((700, 129, 1), 8, 2, 128, BF16, 100, 0, False, seed=1),
+             Case((64, 1, 37), 4, 2, 16, F32, 9, 3, False, seed=4)]
+    wants = []
+    for c in cases:
+        o, lse = c.forward(pha)
+        wants.append((o, lse, c.backward(pha, o, lse)))
+    fwd = max((c.workspace(pha) for c in cases), key=lambda w: w.numel())
+    sizes = [pha.pha_attn_sinks_bwd_workspace_bytes(c.shape[0], c.shape[1], c.q.shape[0], *c.shape[2:], **c.kw)
+             for c in cases]
+    bwd = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty_like(x) for x in (o, lse, *g)] for o, lse, g in wants]
+
+    def step(i):
+        c, (o, lse, *g) = cases[i], outs[i]
+        pha.pha_attn_sinks_fwd(c.q, c.k, c.v, c.cu, c.max_len, o, lse, fwd, **c.kw)
+        pha.pha_attn_sinks_bwd(c.q, c.k, c.v, o, lse, c.dout, c.cu, c.max_len, *g, bwd, **c.kw)
+
+    graphs = []
+    for i in range(len(cases)):
+        step(i)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(i)
+        graphs.append(g)
+    for turn in range(3):
+        for i in (0, 1, 2, 3, 4, 0, 3, 2, 1, 4, 2, 2, 0):
+            for x in outs[i]:
+                x.fill_(float("nan"))
+            graphs[i].replay() if (turn + i) % 2 else step(i)
+            for got, want in zip(outs[i], (wants[i][0], wants[i][1], *wants[i][2])):
+                assert torch.equal(got, want)

@@ -66,6 +66,8 @@ def _sinks(pha, bwd=False, **kw):
     (dict(v=None), -1),
     (dict(lse=A + 2), -1),
     (dict(cu=None), -1),
+    (dict(total=1 << 24, H=128, Hkv=128), -1),  # more rows than 31 bits count
+    (dict(total=(1 << 24) - 1, H=128, Hkv=128), -3),
 ])
 def test_sinks_argument_errors(pha, bwd, kw, code):
     assert _sinks(pha, bwd, **kw) == code
@@ -98,6 +100,8 @@ def _paged(pha, **kw):
     (dict(n_pages=0), -1),
     (dict(max_pages=0), -1),
     (dict(n_pages=1 << 27, page=16), -1),      # more rows than 31 bits count
+    (dict(total=1 << 24, H=128, Hkv=4), -1),
+    (dict(total=(1 << 24) - 1, H=128, Hkv=4), -3),
     (dict(sinks=-1), -1),
     (dict(sinks=1000, window=5), -3),
     (dict(hd=96), -2),
