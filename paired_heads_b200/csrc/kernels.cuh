@@ -180,7 +180,7 @@ cudaError_t launch_attn_bwd_tc(const AttnProblem& p, const CUtensorMap& tm_q,
                                WorkspaceHeader* hdr, int which, cudaStream_t stream);
 
 // Backward with window and sinks (bf16, head_dim 64 / 128; p.sinks, p.window may be 0): -lse log2(e) and
-// -D of every row into nlse, nd (float[slots][heads]); then dQ over a kSchedTilesQ list, dK / dV over a
+// -D of every row into nlse, nd (float[slots][heads]), beside the work lists launched just before; then dQ over a kSchedTilesQ list, dK / dV over a
 // kSchedTilesK list (with far pieces, summed at the end). Maps as launch_attn_bwd_tc.
 cudaError_t launch_attn_bwd_sinks_rows(const AttnProblem& p, const void* o, const void* dout,
                                        float* nlse, float* nd, cudaStream_t stream);
@@ -208,9 +208,11 @@ cudaError_t launch_qk_norm_rope(void* q, void* k, const float* q_weight, const f
 cudaError_t launch_attn_f32(const AttnProblem& p, cudaStream_t stream);
 
 // Builds the varlen work list of the given shape into `items` (capacity entries) and the header;
-// doc_blocks is int32[batch + 1] scratch.
+// doc_blocks is int32[batch + 1] scratch. beside: the launch before it on the stream was of another
+// list, and this one is built at the same time.
 cudaError_t launch_schedule(const AttnProblem& p, ScheduleMode mode, int capacity, int* doc_blocks,
-                            int4* items, WorkspaceHeader* hdr, cudaStream_t stream);
+                            int4* items, WorkspaceHeader* hdr, cudaStream_t stream,
+                            bool beside = false);
 
 // tcgen05 attention over a scheduled work list. tm_q / tm_k / tm_v are 2-D bf16 tensor maps
 // over the slot view ([slots][heads * head_dim] and [slots][kv_heads * head_dim]) with a

@@ -211,18 +211,18 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
     auto* hdr = reinterpret_cast<WorkspaceHeader*>(base);
     auto* hdr_k = reinterpret_cast<WorkspaceHeader*>(base + w.keys);
     auto list = [&](size_t at) { return reinterpret_cast<int4*>(base + at + w.list); };
-    auto build = [&](ScheduleMode mode, size_t at, int64_t items) {
+    auto build = [&](ScheduleMode mode, size_t at, int64_t items, bool beside) {
         return launch_schedule(p, mode, items < INT32_MAX ? static_cast<int>(items) : INT32_MAX,
                                reinterpret_cast<int*>(base + at + kWorkspaceHeaderBytes), list(at),
-                               reinterpret_cast<WorkspaceHeader*>(base + at), stream);
+                               reinterpret_cast<WorkspaceHeader*>(base + at), stream, beside);
     };
     float* dsum = reinterpret_cast<float*>(base + w.dsum);
     p.sink_part = reinterpret_cast<float*>(base + w.part);
     p.checked = hdr;
     const bool tc = dtype == PHA_BF16;
-    // the scheduler also checks cu_seqlens; without a list to walk (CUDA cores) only that is used
-    if (build(kSchedTilesQ, 0, w.items_q) != cudaSuccess) return PHA_ERR_CUDA;
     if (!tc) {
+        // the scheduler also checks cu_seqlens; without a list to walk (CUDA cores) only that is used
+        if (build(kSchedTilesQ, 0, w.items_q, false) != cudaSuccess) return PHA_ERR_CUDA;
         if (launch_attn_bwd_dsum(p, o, dout, dsum, 0, stream) != cudaSuccess) return PHA_ERR_CUDA;
         return of(launch_attn_bwd(p, dout, dsum, dq, dk, dv, 0, stream));
     }
@@ -235,11 +235,13 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
         !encode_slot_map(&tdq, dq, wq, rows, 32) || !encode_slot_map(&tdk, dk, wk, rows, 16) ||
         !encode_slot_map(&tdv, dv, wk, rows, 16))
         return PHA_ERR_CUDA;
+    // both lists and the rows' sums at the same time
     if (launch_attn_bwd_zero_outside(p, dq, dk, dv, stream) != cudaSuccess ||
+        build(kSchedTilesQ, 0, w.items_q, false) != cudaSuccess ||
+        build(kSchedTilesK, w.keys, w.items_k, true) != cudaSuccess ||
         launch_attn_bwd_sinks_rows(p, o, dout, nlse, dsum, stream) != cudaSuccess ||
         launch_attn_bwd_sinks_dq(p, tq, tk, tv, tdo, tdq, nlse, dsum, dq, list(0), hdr, &hdr->status,
-                                 stream) != cudaSuccess ||
-        build(kSchedTilesK, w.keys, w.items_k) != cudaSuccess)
+                                 stream) != cudaSuccess)
         return PHA_ERR_CUDA;
     return of(launch_attn_bwd_sinks_dkdv(p, tq, tk, tv, tdo, tdk, tdv, nlse, dsum, dk, dv, list(w.keys), hdr_k,
                                          &hdr->status, stream));  // (one status word for the call)

@@ -170,11 +170,9 @@ __device__ __forceinline__ BlockRange block_range(const AttnProblem& p, int64_t 
     return r;
 }
 
-__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnProblem p, int capacity,
-                                                                 int n_buckets, int mode,
-                                                                 int* __restrict__ doc_blocks,
-                                                                 int4* __restrict__ items,
-                                                                 WorkspaceHeader* hdr) {
+__device__ __forceinline__ void build_schedule(const AttnProblem& p, int capacity, int n_buckets, int mode,
+                                               int* __restrict__ doc_blocks, int4* __restrict__ items,
+                                               WorkspaceHeader* hdr) {
     __shared__ int hist[kMaxCostBuckets];
     __shared__ int warp_sums[kSchedThreads / 32];
     __shared__ int bad;
@@ -309,6 +307,15 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnProblem p, 
     }
 }
 
+__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnProblem p, int capacity,
+                                                                 int n_buckets, int mode,
+                                                                 int* __restrict__ doc_blocks,
+                                                                 int4* __restrict__ items,
+                                                                 WorkspaceHeader* hdr) {
+    build_schedule(p, capacity, n_buckets, mode, doc_blocks, items, hdr);
+    grid_dep_wait();  // beside another list: this grid's end is the end of both
+}
+
 int schedule_buckets(const AttnProblem& p, int mode) {
     if (mode == kSchedBand) return kBandTiles + 2;
     if (mode == kSchedTilesQ || mode == kSchedTilesK) {
@@ -321,10 +328,18 @@ int schedule_buckets(const AttnProblem& p, int mode) {
 }
 
 cudaError_t launch_schedule(const AttnProblem& p, ScheduleMode mode, int capacity, int* doc_blocks,
-                            int4* items, WorkspaceHeader* hdr, cudaStream_t stream) {
-    schedule_kernel<<<1, kSchedThreads, 0, stream>>>(p, capacity, schedule_buckets(p, mode),
-                                                     static_cast<int>(mode), doc_blocks, items, hdr);
-    return cudaGetLastError();
+                            int4* items, WorkspaceHeader* hdr, cudaStream_t stream, bool beside) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kSchedThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, schedule_kernel, p, capacity, schedule_buckets(p, mode),
+                              static_cast<int>(mode), doc_blocks, items, hdr);
 }
 
 }  // namespace pha
