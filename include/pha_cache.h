@@ -31,9 +31,9 @@ extern "C" {
 
 /*
  * pha_attn_paged_workspace_bytes -- device workspace of pha_attn_paged_fwd with the same arguments
- *   (work list, partial results of split key ranges). 0 for invalid arguments. It grows with each
- *   of batch, max_q, max_kv and total_q, except that more rows can need fewer splits: a workspace
- *   kept for varying steps has the largest size among them.
+ *   (work list, partial results of split key ranges). 0 for invalid arguments. The number of ranges
+ *   follows the shape, so the size does not grow with every argument: a workspace kept for varying
+ *   steps has the largest size among them.
  */
 size_t pha_attn_paged_workspace_bytes(int batch, int max_q, int max_kv, int total_q, int n_heads,
                                       int n_kv_heads, int head_dim, pha_dtype dtype, int window,
