@@ -23,7 +23,7 @@
 // are computed; while the next stage A runs, dK += dS^T Q and the next dP. (Both stages after both
 // products, as in attn_bwd_tc.cu: 798 us for dK / dV of 2 x 8192 tokens, 32 / 8 heads of 128, window
 // 1024, 675 for dQ; the two column halves of a step staggered instead: 680 and 574, the halves' N = 64
-// products reading X twice; this one: 637 and 441, 4,400 and 3,000 clocks a step.) What is left over the
+// products reading X twice; this one: 530 and 367, 3,700 and 2,500 clocks a step.) What is left over the
 // products' 2,050 and 1,540 clocks is the chain S -> P -> dV -> next S, P lying in S's columns: with 256
 // columns of accumulators TMEM has no room for a second S.
 // TMEM columns: S [0, 128), dP [128, 256), accumulators from 256 (dV, dK or dQ). Key-major, P^T and dS^T
@@ -35,8 +35,11 @@
 //   warps 0-7   two warpgroups, warpgroup h taking columns 64 h .. 64 h + 63 of every step (row = TMEM
 //               lane) and half h of the accumulator columns in the epilogue
 //   warp 8      issues the second products (dV and dK, or dQ)
-//   warp 9      issues the first products (S and dP); owner of the 512 TMEM columns. (One thread for all
-//               four products spent 2,500 of 5,200 clocks a step between them.)
+//   warp 9      issues the first products (S and dP); owner of the 512 TMEM columns. (One warp for all
+//               four products spent 2,500 of 5,200 clocks a step between them.) Both run as whole warps,
+//               with an elected lane for the MMAs alone and a warp index that is uniform to the compiler:
+//               the MMAs' operands then stay in uniform registers. (Under `if (lane == 0)` an MMA took about
+//               100 clocks to issue: 637 us instead of 575 for dK / dV, 443 instead of 377 for dQ.)
 //   warp 10     producer: X and Y tiles by TMA, key-major also -lse log2(e) and -D of the queries
 //   warp 11     blanks the rows of a landed Y tile that lie behind the document's end: whatever is there (a
 //               padded batch's NaN) would meet a zero weight, and 0 * NaN is NaN
@@ -86,8 +89,8 @@ struct Layout {
 // y0_full or y0_ok), and of each outer tile (four of them: a step three before a tile's first one belongs
 // at the latest to the tile three before it, so everybody has left the one four before). The other roles
 // decode nothing: their code has to stay small beside the elementwise loops, whose instructions it pushes
-// out of the cache (each role walking the list by itself: 656 us instead of 637 for dK / dV, 496 instead
-// of 441 for dQ, 2 x 8192 tokens, 32 / 8 heads of 128, window 1024).
+// out of the cache (each role walking the list by itself, before other changes: 656 us instead of 637 for dK / dV,
+// 496 instead of 441 for dQ, 2 x 8192 tokens, 32 / 8 heads of 128, window 1024).
 struct StepRec {
     int flags;  // kFirst, kLast step of its outer tile; kEnd: no step, the list is done
     int y_row;  // first slot of the Y tiles
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* vec = reinterpret_cast<float*>(smem + L::kOffVec);
     volatile int* abort_flag = &bars->abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (uniform)
     const int lane = threadIdx.x & 31;
 
     if (warp == 8 && lane == 0) {
@@ -410,111 +413,127 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 9) {
         // ------------------------------------------------------------ the products S and dP
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (ok) ok = mbar_wait(bar, parity, abort_flag, dev_status);
-            };
-            // d = X_w times Y (both K-major), the first `cols` columns
-            auto product = [&](uint32_t d, int w, int y_off, int cols, uint64_t* full) {
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t id = KEYMAJOR ? idesc : (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(cols >> 3) << 17);
-                const uint64_t dx = desc_kmajor(sbase + L::kOffX + w * L::kTile, 0);
-                const uint64_t dy = desc_kmajor(sbase + y_off, 0);
+        constexpr uint32_t idesc = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
+        };
+        // d = X_w times Y (both K-major), the first `cols` columns
+        auto product = [&](uint32_t d, int w, int y_off, int cols, uint64_t* full) {
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t id = KEYMAJOR ? idesc : (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(cols >> 3) << 17);
+            const uint64_t dx = desc_kmajor(sbase + L::kOffX + w * L::kTile, 0);
+            const uint64_t dy = desc_kmajor(sbase + y_off, 0);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {  // (as desc_kmajor steps)
                     const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                     umma_f16_ss(d, dx + step, dy + step, id, kk == 0 ? 0u : 1u);
                 }
                 umma_commit(full);
-            };
-            Ring<L::kR0> y0;
-            uint32_t tiles = 0;
-            for (uint32_t g = 0; ok; ++g) {
-                wait(&bars->y0_ok[y0.i], y0.lap);
-                if (!ok) break;
-                const int flags = bars->step[y0.i].flags, cols = bars->step[y0.i].cols;
-                if (flags & kEnd) break;
-                if (flags & kFirst) {
-                    wait(&bars->x_full, tiles & 1);
-                    ++tiles;
-                }
-                // S, when its columns are free: key-major P lay in them (dV's product), query-major once read
-                if (g > 0) wait(KEYMAJOR ? &bars->m2_done[0] : &bars->a_done, (g - 1) & 1);
-                product(tmem + L::kTmS, 0, L::kOffY0 + y0.i * L::kTile, cols, &bars->s_full);
-                // dP, likewise (dS lay in its columns)
-                wait(&bars->y1_ok, g & 1);
-                if (g > 0) wait(KEYMAJOR ? &bars->m2_done[1] : &bars->dp_read, (g - 1) & 1);
-                product(tmem + L::kTmDP, 1, L::kOffY1, cols, &bars->dp_full);
-                if (!ok) break;
+            }
+            __syncwarp();
+        };
+        Ring<L::kR0> y0;
+        uint32_t tiles = 0;
+        for (uint32_t g = 0; ok; ++g) {
+            wait(&bars->y0_ok[y0.i], y0.lap);
+            if (!ok) break;
+            const int flags = __shfl_sync(0xffffffffu, bars->step[y0.i].flags, 0);
+            const int cols = __shfl_sync(0xffffffffu, bars->step[y0.i].cols, 0);
+            if (flags & kEnd) break;
+            if (flags & kFirst) {
+                wait(&bars->x_full, tiles & 1);
+                ++tiles;
+            }
+            // S, when its columns are free: key-major P lay in them (dV's product), query-major once read
+            if (g > 0) wait(KEYMAJOR ? &bars->m2_done[0] : &bars->a_done, (g - 1) & 1);
+            product(tmem + L::kTmS, 0, L::kOffY0 + y0.i * L::kTile, cols, &bars->s_full);
+            // dP, likewise (dS lay in its columns)
+            wait(&bars->y1_ok, g & 1);
+            if (g > 0) wait(KEYMAJOR ? &bars->m2_done[1] : &bars->dp_read, (g - 1) & 1);
+            product(tmem + L::kTmDP, 1, L::kOffY1, cols, &bars->dp_full);
+            if (!ok) break;
+            if (elect_one()) {
                 umma_commit(&bars->y1_empty);
                 if (flags & kLast) umma_commit(&bars->x_empty);
-                y0.next();
             }
-            // Wait (bounded) until every MMA this thread issued has finished.
-            umma_commit(&bars->drain[0]);
-            drain_wait(&bars->drain[0], 0);
+            __syncwarp();
+            y0.next();
         }
+        // Wait (bounded) until every MMA this warp issued has finished.
+        if (elect_one()) umma_commit(&bars->drain[0]);
         __syncwarp();
+        drain_wait(&bars->drain[0], 0);
     } else if (warp == 8) {
         // ------------------------------------------------------------ the products dV and dK, or dQ
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kBlockM, HD, 0, 1);
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (ok) ok = mbar_wait(bar, parity, abort_flag, dev_status);
-            };
-            // acc (+)= A (TMEM, bf16 pairs; column half h at a + h * half) times Y's rows (MN-major)
-            auto product = [&](uint32_t acc, uint32_t a, uint32_t half, int y_off, bool first, int cols) {
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t dy = desc_v(sbase + y_off, 0);
+        constexpr uint32_t idesc = idesc_bf16_f32(kBlockM, HD, 0, 1);
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
+        };
+        // acc (+)= A (TMEM, bf16 pairs; column half h at a + h * half) times Y's rows (MN-major)
+        auto product = [&](uint32_t acc, uint32_t a, uint32_t half, int y_off, bool first, int cols) {
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t dy = desc_v(sbase + y_off, 0);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kBlockN / 16; ++kk) {
                     if (!KEYMAJOR && 16 * kk >= cols) continue;
                     umma_f16_ts(acc, a + (kk >> 2) * half + (kk & 3) * 8, dy + kk * (2048 >> 4), idesc,
                                 (!first || kk > 0) ? 1u : 0u);
                 }
-            };
-            Ring<L::kR0> y0;
-            uint32_t tiles = 0;
-            for (uint32_t g = 0; ok; ++g) {
-                wait(&bars->y0_ok[y0.i], y0.lap);
+            }
+            __syncwarp();
+        };
+        Ring<L::kR0> y0;
+        uint32_t tiles = 0;
+        for (uint32_t g = 0; ok; ++g) {
+            wait(&bars->y0_ok[y0.i], y0.lap);
+            if (!ok) break;
+            const int flags = __shfl_sync(0xffffffffu, bars->step[y0.i].flags, 0);
+            const int cols = __shfl_sync(0xffffffffu, bars->step[y0.i].cols, 0);
+            if (flags & kEnd) break;
+            const bool first = (flags & kFirst) != 0;
+            const int y0_off = L::kOffY0 + y0.i * L::kTile;
+            wait(KEYMAJOR ? &bars->a_done : &bars->b_done, g & 1);
+            if (first) {
+                if (tiles > 0) wait(&bars->acc_empty, (tiles - 1) & 1);
+                ++tiles;
+            }
+            if (KEYMAJOR) {
+                wait(&bars->y1_ok, g & 1);  // (P needs S alone: dO may still be on its way)
+                product(tmem + L::kTmAcc, tmem + L::kTmS, 64, L::kOffY1, first, kBlockN);
                 if (!ok) break;
-                const int flags = bars->step[y0.i].flags, cols = bars->step[y0.i].cols;
-                if (flags & kEnd) break;
-                const bool first = (flags & kFirst) != 0;
-                const int y0_off = L::kOffY0 + y0.i * L::kTile;
-                wait(KEYMAJOR ? &bars->a_done : &bars->b_done, g & 1);
-                if (first) {
-                    if (tiles > 0) wait(&bars->acc_empty, (tiles - 1) & 1);
-                    ++tiles;
-                }
-                if (KEYMAJOR) {
-                    wait(&bars->y1_ok, g & 1);  // (P needs S alone: dO may still be on its way)
-                    product(tmem + L::kTmAcc, tmem + L::kTmS, 64, L::kOffY1, first, kBlockN);
-                    if (!ok) break;
+                if (elect_one()) {
                     umma_commit(&bars->m2_done[0]);
                     umma_commit(&bars->y1_empty);
-                    wait(&bars->b_done, g & 1);
-                    product(tmem + L::kTmAcc + HD, tmem + L::kTmDP, 64, y0_off, first, kBlockN);
-                    if (!ok) break;
-                    umma_commit(&bars->m2_done[1]);
-                } else {
-                    product(tmem + L::kTmAcc, tmem + L::kTmDS + 64 * (g & 1), 32, y0_off, first, cols);
-                    if (!ok) break;
-                    umma_commit(&bars->m2_done[g & 1]);
                 }
+                __syncwarp();
+                wait(&bars->b_done, g & 1);
+                // behind the next S, which the next stage A waits for (before it: 557 us instead of 530);
+                // not at a tile's end, where that S waits for X
+                if (!(flags & kLast)) wait(&bars->s_full, (g + 1) & 1);
+                product(tmem + L::kTmAcc + HD, tmem + L::kTmDP, 64, y0_off, first, kBlockN);
+                if (!ok) break;
+                if (elect_one()) umma_commit(&bars->m2_done[1]);
+            } else {
+                product(tmem + L::kTmAcc, tmem + L::kTmDS + 64 * (g & 1), 32, y0_off, first, cols);
+                if (!ok) break;
+                if (elect_one()) umma_commit(&bars->m2_done[g & 1]);
+            }
+            if (elect_one()) {
                 umma_commit(&bars->y0_empty[y0.i]);
                 if (flags & kLast) umma_commit(&bars->acc_full);
-                y0.next();
             }
-            umma_commit(&bars->drain[1]);
-            drain_wait(&bars->drain[1], 0);
+            __syncwarp();
+            y0.next();
         }
+        if (elect_one()) umma_commit(&bars->drain[1]);
         __syncwarp();
+        drain_wait(&bars->drain[1], 0);
     } else {
         // ------------------------------------------------------------ elementwise warpgroups
         regs_increase<kRegsElementwise>();

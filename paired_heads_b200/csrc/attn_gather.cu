@@ -20,7 +20,11 @@
 //               a whole warp skip their exponentials), P (bf16) to TMEM, O rescaled there only when the
 //               maximum grew by more than 2^8
 //   warp 8      MMA issuer and TMEM owner: S_r = Q_r K^T, O_r += P_r V, software-pipelined over the
-//               two sub-tiles (P V of the tile before, then S of this one)
+//               two sub-tiles (P V of the tile before, then S of this one). A whole warp with an elected
+//               lane for the MMAs, its index and branches uniform to the compiler, so that the MMAs'
+//               operands stay in uniform registers (under `if (lane == 0)`: 260 us instead of 202 for 4 x
+//               8192 tokens, 12 heads of 64, window 1024, 16 sinks; 324 instead of 304 for 2 x 8192, 32 / 8
+//               heads of 128)
 //   warps 9-11  loaders: plain key tiles by TMA (K: warp 9, V: warp 10, a lane per box), Q too where
 //               `pack` divides 128; gathered tiles and other Q by 16-byte cp.async into the same
 //               128-byte-swizzled layout, its completion signalled by the copies themselves
@@ -42,10 +46,10 @@ namespace {
 
 constexpr int kLoadWarps = 3;
 // Register split: the softmax rows need all they can get (a spill in their loop goes to L2, the shared
-// memory leaves no L1 to speak of, and cost 1.6 times the time); 8 x 200 + 4 x 104 warps' shares use up
+// memory leaves no L1 to speak of, and cost 1.6 times the time); 8 x 216 + 4 x 72 warps' shares use up
 // the launch's 12 x 168.
-constexpr int kRegsSoftmax = 200;
-constexpr int kRegsOther = 104;
+constexpr int kRegsSoftmax = 216;
+constexpr int kRegsOther = 72;
 static_assert(8 * kRegsSoftmax + 4 * kRegsOther <= 12 * 168, "register split");
 
 // A segment: the key tiles [tb, te) of one row tile and head chunk, and what each sub-tile uses of
@@ -165,7 +169,7 @@ __device__ __forceinline__ GItem decode_gather(const GWalk& wk, const GatherProb
 
 // What the MMA issuer and the softmax warps need of a segment, written by loader warp 9 as it reaches
 // it, well ahead of them. (Each role decoding for itself put a few hundred instructions, cold in the
-// instruction cache, between two items: 4,000 cycles in the MMA thread, 2,200 in the softmax warps.)
+// instruction cache, between two items: 4,000 cycles in the MMA warp, 2,200 in the softmax warps.)
 struct GBoard {
     int last_one;  // the share is over; nothing else is valid
     int q0, chunk, pos0, tb, te, whole, begins, lo, n_w, total, ns, sf, sl;
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int* abort_flag = &bars->abort;
     int* dev_status = &p.hdr->status;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (uniform)
     const int lane = threadIdx.x & 31;
 
     if (warp == 8) {
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             for (uint32_t i = 0; i < kBoards; ++i) {
                 mbar_init(&gbars->item_full[i], 1);
-                mbar_init(&gbars->item_empty[i], 9);  // the MMA thread and 8 softmax warps
+                mbar_init(&gbars->item_empty[i], 9);  // the MMA warp and 8 softmax warps
             }
             mbar_init(&bars->drain, 1);
             bars->abort = 0;
@@ -436,91 +440,94 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, HD, 0, 1);
-            uint32_t s_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};  // S and P V products issued per sub-tile
-            bool pv_open[2] = {false, false};  // hd 128: the last P V of r not yet seen complete
-            // key tile g - 1 as sub-tile r used it: its S was issued, its P V not yet
-            bool pend[2] = {false, false}, pend_first[2] = {false, false}, pend_last[2] = {false, false};
-            uint32_t qc = 0;  // Q sub-tiles of the segments before the current one
-            uint32_t g = 0;   // index of the current key tile in this CTA's stream
-            bool ok = true, more = true;
-            for (uint32_t ic = 0; ok && more; ++ic) {
-                const uint32_t ib = ic % kBoards;
-                if (!mbar_wait(&gbars->item_full[ib], (ic / kBoards) & 1, abort_flag, dev_status)) {
-                    ok = false;
-                    break;
-                }
-                const GBoard& bd = gbars->board[ib];
-                more = !bd.last_one;  // behind the last segment: one more turn, for the last P V
-                const int tb = more ? bd.tb : 0, te = more ? bd.te : (g > 0 ? 1 : 0), sf = bd.sf, sl = bd.sl;
-                int nr[2], wf[2], wl[2], first[2], last[2];
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, HD, 0, 1);
+        uint32_t s_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};  // S and P V products issued per sub-tile
+        bool pv_open[2] = {false, false};  // hd 128: the last P V of r not yet seen complete
+        // key tile g - 1 as sub-tile r used it: its S was issued, its P V not yet
+        bool pend[2] = {false, false}, pend_first[2] = {false, false}, pend_last[2] = {false, false};
+        uint32_t qc = 0;  // Q sub-tiles of the segments before the current one
+        uint32_t g = 0;   // index of the current key tile in this CTA's stream
+        bool ok = true, more = true;
+        for (uint32_t ic = 0; ok && more; ++ic) {
+            const uint32_t ib = ic % kBoards;
+            ok = __all_sync(0xffffffffu, mbar_wait(&gbars->item_full[ib], (ic / kBoards) & 1, abort_flag, dev_status));
+            if (!ok) break;
+            const GBoard& bd = gbars->board[ib];
+            auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+            more = !uniform(bd.last_one);  // behind the last segment: one more turn, for the last P V
+            const int tb = more ? uniform(bd.tb) : 0, te = more ? uniform(bd.te) : (g > 0 ? 1 : 0);
+            const int sf = uniform(bd.sf), sl = uniform(bd.sl);
+            int nr[2], wf[2], wl[2], first[2], last[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    nr[r] = bd.nr[r];
-                    wf[r] = bd.wf[r];
-                    wl[r] = bd.wl[r];
-                    first[r] = bd.first[r];
-                    last[r] = bd.last[r];
-                }
-                mbar_arrive(&gbars->item_empty[ib]);
-                uint32_t q_slot[2], q_par[2], n_act = 0;
+            for (int r = 0; r < 2; ++r) {
+                nr[r] = uniform(bd.nr[r]);
+                wf[r] = uniform(bd.wf[r]);
+                wl[r] = uniform(bd.wl[r]);
+                first[r] = uniform(bd.first[r]);
+                last[r] = uniform(bd.last[r]);
+            }
+            if (lane == 0) mbar_arrive(&gbars->item_empty[ib]);
+            uint32_t q_slot[2], q_par[2], n_act = 0;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    q_slot[r] = (qc + n_act) % L::kQSlots;
-                    q_par[r] = ((qc + n_act) / L::kQSlots) & 1;
-                    n_act += more && first[r] <= last[r] ? 1 : 0;
+            for (int r = 0; r < 2; ++r) {
+                q_slot[r] = (qc + n_act) % L::kQSlots;
+                q_par[r] = ((qc + n_act) / L::kQSlots) & 1;
+                n_act += more && first[r] <= last[r] ? 1 : 0;
+            }
+            qc += n_act;
+            for (int t = tb; t < te; ++t) {
+                if (g > 0) {
+                    const uint32_t n = g - 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[n % L::kVStages], (n / L::kVStages) & 1, abort_flag, dev_status));
+                    if (!ok) break;
+                    fence_proxy_async_smem();  // gathered rows were written by cp.async; the MMA reads them next
                 }
-                qc += n_act;
-                for (int t = tb; t < te; ++t) {
-                    if (g > 0) {
-                        const uint32_t n = g - 1;
-                        ok = mbar_wait(&bars->v_full[n % L::kVStages], (n / L::kVStages) & 1, abort_flag, dev_status);
-                        if (!ok) break;
-                        fence_proxy_async_smem();  // gathered rows were written by cp.async; the MMA reads them next
-                    }
-                    const uint32_t sk = g % L::kKStages;
-                    if (more) {
-                        ok = mbar_wait(&bars->k_full[sk], (g / L::kKStages) & 1, abort_flag, dev_status);
-                        if (!ok) break;
-                        fence_proxy_async_smem();
-                    }
-                    // O_r += P_r V_{g-1}
-                    auto product_pv = [&](int r, bool is_first, bool is_last) {
-                        ok = mbar_wait(&bars->p_full[r], p_cnt[r] & 1, abort_flag, dev_status);
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint32_t a_p = tmem + (kSepP ? kTmP + 64 * r : 128 * r);
-                        const uint64_t v0 = desc_v(sbase + L::kOffV + ((g - 1) % L::kVStages) * L::kKV, 0);
+                const uint32_t sk = g % L::kKStages;
+                if (more) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[sk], (g / L::kKStages) & 1, abort_flag, dev_status));
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                }
+                // O_r += P_r V_{g-1}
+                auto product_pv = [&](int r, bool is_first, bool is_last) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[r], p_cnt[r] & 1, abort_flag, dev_status));
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t a_p = tmem + (kSepP ? kTmP + 64 * r : 128 * r);
+                    const uint64_t v0 = desc_v(sbase + L::kOffV + ((g - 1) % L::kVStages) * L::kKV, 0);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBlockN / 16; ++kk)  // 2048 bytes on per 16 keys
                             umma_f16_ts(tmem + L::kTmO + HD * r, a_p + 8 * kk, v0 + kk * (2048 >> 4), idesc_pv,
                                         (!is_first || kk > 0) ? 1u : 0u);
                         umma_commit(&bars->pv_done[r]);
                         if (is_last) umma_commit(&bars->o_ready[r]);
-                        ++p_cnt[r];
-                        pv_open[r] = !kSepP;
-                    };
-                    // S_r = Q_r K_g^T
-                    auto product_s = [&](int r) {
-                        if (kSepP) {
-                            // hd 64: S_r is free once the softmax has read its last tile
-                            if (s_cnt[r] > 0)
-                                ok = mbar_wait(&bars->s_free[r], (s_cnt[r] - 1) & 1, abort_flag, dev_status);
-                        } else if (pv_open[r]) {
-                            // hd 128: S_r overwrites the columns that P_r shares with it
-                            ok = mbar_wait(&bars->pv_done[r], (p_cnt[r] - 1) & 1, abort_flag, dev_status);
-                            pv_open[r] = false;
-                        }
-                        if (ok && t == first[r]) {
-                            ok = mbar_wait(&bars->q_full[q_slot[r]], q_par[r], abort_flag, dev_status);
-                            fence_proxy_async_smem();
-                        }
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint64_t q0 = desc_kmajor(sbase + L::kOffQ + q_slot[r] * L::kQSub, 0);
-                        const uint64_t k0 = desc_kmajor(sbase + L::kOffK + sk * L::kKV, 0);
+                    }
+                    __syncwarp();
+                    ++p_cnt[r];
+                    pv_open[r] = !kSepP;
+                };
+                // S_r = Q_r K_g^T
+                auto product_s = [&](int r) {
+                    if (kSepP) {
+                        // hd 64: S_r is free once the softmax has read its last tile
+                        if (s_cnt[r] > 0)
+                            ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_free[r], (s_cnt[r] - 1) & 1, abort_flag, dev_status));
+                    } else if (pv_open[r]) {
+                        // hd 128: S_r overwrites the columns that P_r shares with it
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[r], (p_cnt[r] - 1) & 1, abort_flag, dev_status));
+                        pv_open[r] = false;
+                    }
+                    if (ok && t == first[r]) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[q_slot[r]], q_par[r], abort_flag, dev_status));
+                        fence_proxy_async_smem();
+                    }
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t q0 = desc_kmajor(sbase + L::kOffQ + q_slot[r] * L::kQSub, 0);
+                    const uint64_t k0 = desc_kmajor(sbase + L::kOffK + sk * L::kKV, 0);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk) {  // (as desc_kmajor steps)
                             const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
@@ -528,35 +535,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         umma_commit(&bars->s_full[r]);
                         if (t == last[r]) umma_commit(&bars->q_empty[q_slot[r]]);
-                        ++s_cnt[r];
-                        pend[r] = true;
-                        pend_first[r] = t == first[r];
-                        pend_last[r] = t == last[r];
-                    };
-                    // Sub-tile by sub-tile; hd 64: S, then P V of the tile before; hd 128 (P over S): the other
-                    // way round. A segment's first S_1 may have to wait for the epilogue of the last one's
-                    // sub-tile 0 (its Q slot), whose P V comes before it here. One copy of each product:
-                    // this thread's code is fetched anew whenever the softmax loop has pushed it out.
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const bool uses = more && nr[r] > 0 && ((t >= wf[r] && t <= wl[r]) || (t >= sf && t <= sl));
-                        const bool pv = pend[r], pv_first = pend_first[r], pv_last = pend_last[r];
-                        pend[r] = false;
-                        if (kSepP && ok && uses) product_s(r);
-                        if (ok && pv) product_pv(r, pv_first, pv_last);
-                        if (!kSepP && ok && uses) product_s(r);
                     }
-                    if (!ok || !more) break;
+                    __syncwarp();
+                    ++s_cnt[r];
+                    pend[r] = true;
+                    pend_first[r] = t == first[r];
+                    pend_last[r] = t == last[r];
+                };
+                // Sub-tile by sub-tile; hd 64: S, then P V of the tile before; hd 128 (P over S): the other
+                // way round. A segment's first S_1 may have to wait for the epilogue of the last one's
+                // sub-tile 0 (its Q slot), whose P V comes before it here. One copy of each product:
+                // this warp's code is fetched anew whenever the softmax loop has pushed it out.
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const bool uses = more && nr[r] > 0 && ((t >= wf[r] && t <= wl[r]) || (t >= sf && t <= sl));
+                    const bool pv = pend[r], pv_first = pend_first[r], pv_last = pend_last[r];
+                    pend[r] = false;
+                    if (kSepP && ok && uses) product_s(r);
+                    if (ok && pv) product_pv(r, pv_first, pv_last);
+                    if (!kSepP && ok && uses) product_s(r);
+                }
+                if (!ok || !more) break;
+                if (elect_one()) {
                     if (g > 0) umma_commit(&bars->v_empty[(g - 1) % L::kVStages]);
                     umma_commit(&bars->k_empty[sk]);
-                    ++g;
                 }
+                __syncwarp();
+                ++g;
             }
-            // Wait (bounded) until every MMA this thread issued has finished.
-            umma_commit(&bars->drain);
-            drain_wait(&bars->drain, 0);
         }
+        // Wait (bounded) until every MMA this warp issued has finished.
+        if (elect_one()) umma_commit(&bars->drain);
         __syncwarp();
+        drain_wait(&bars->drain, 0);
     } else {
         // ------------------------------------------------------------ softmax, sub-tile r
         regs_increase<kRegsSoftmax>();

@@ -224,6 +224,17 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// One lane of a whole warp (always the same one within a kernel's warp): true there, false elsewhere.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16; A (M x 16) sits in TMEM as packed bf16 pairs, row m
 // in lane m, 8 columns per 16 elements of K.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
