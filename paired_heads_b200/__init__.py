@@ -2,7 +2,8 @@
 attention, including the paired-head variant of the modded-nanogpt "Paired Head Attention" record.
 
 The compute lives in the C-ABI library ``libpha.so`` (hand-written sm_100a CUDA, declared in
-``include/pha.h``). ``paired_heads_b200.pha`` is the thin ctypes binding over it; importing it
+``include/pha.h``; window attention with sinks in ``include/pha_sinks.h``, the paged cache in
+``include/pha_cache.h``). ``paired_heads_b200.pha`` is the thin ctypes binding over it; importing it
 fails loudly if the library is missing. ``paired_heads_b200.synth`` draws the seeded synthetic
 workloads. Importing this package itself loads nothing.
 """

@@ -16,13 +16,12 @@
 //
 // CTA = 12 warps, one per SM, each with an equal share of all key tiles (gather_plan.cu):
 //   warps 0-7   softmax, a warpgroup per sub-tile, thread = row = TMEM lane: the 128 scores in
-//               registers, hidden ones set to -inf from a bit mask per 32 columns (chunks hidden from
-//               a whole warp skip their exponentials), P (bf16) to TMEM, O rescaled there only when the
-//               maximum grew by more than 2^8
+//               registers, hidden ones set to -inf from a bit mask per 32 columns, P (bf16) to TMEM, O
+//               rescaled there only when the maximum grew by more than 2^8
 //   warp 8      MMA issuer and TMEM owner: S_r = Q_r K^T, O_r += P_r V, software-pipelined over the
 //               two sub-tiles (P V of the tile before, then S of this one). A whole warp with an elected
 //               lane for the MMAs, its index and branches uniform to the compiler, so that the MMAs'
-//               operands stay in uniform registers (under `if (lane == 0)`: 260 us instead of 202 for 4 x
+//               operands stay in uniform registers (under `if (lane == 0)`: 260 us instead of 205 for 4 x
 //               8192 tokens, 12 heads of 64, window 1024, 16 sinks; 324 instead of 304 for 2 x 8192, 32 / 8
 //               heads of 128)
 //   warps 9-11  loaders: plain key tiles by TMA (K: warp 9, V: warp 10, a lane per box), Q too where
@@ -186,14 +185,7 @@ struct GBars {
 constexpr int kGBarBytes = 1280;
 static_assert(sizeof(GBars) <= kGBarBytes, "barrier block");
 
-// Windows up to this run the NARROW form (4 x 8192 tokens, 4 sinks, us, it and the other: 32 / 8 heads of
-// 128, window 64: 148 / 150, 256: 214 / 239, 384: 314 / 320, 1024: 372 / 372; 12 heads of 64, window 128:
-// 150 / 150, 256: 193 / 186, 512: 238 / 219, 1024: 287 / 256).
-constexpr int kNarrowWindow = 256;
-
-// NARROW: windows so short that most tiles are masked; masked tiles then go chunk by
-// chunk and skip the hidden chunks. With long windows the loop's latencies cost more than it skips.
-template <int HD, bool PAGED, bool NARROW>
+template <int HD, bool PAGED>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_gather_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const GatherProblem p, const int p_inv) {
@@ -652,78 +644,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t seen = low_bits(c_hi + 1 - cb) & (~below | low_bits(ns - cb));
                     return seen | (low_bits(total - cb) & ~low_bits(n_w - cb));
                 };
-                if (!NARROW || !masked) {
-                    // the 128 scores at once, in registers
-                    uint32_t v[128];
+                // the 128 scores at once, in registers
+                uint32_t v[128];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, v + 32 * c);
-                    tmem_wait_ld();
+                for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, v + 32 * c);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) regs_after_wait(v + 32 * c);
-                    if (kSepP) {
-                        tc_fence_before();  // S_r may be overwritten from here on
-                        mbar_arrive(&bars->s_free[r]);
-                    }
-                    if (!NARROW && masked) {
-                        uint32_t vis[4];
+                for (int c = 0; c < 4; ++c) regs_after_wait(v + 32 * c);
+                if (kSepP) {
+                    tc_fence_before();  // S_r may be overwritten from here on
+                    mbar_arrive(&bars->s_free[r]);
+                }
+                if (masked) {
+                    uint32_t vis[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) vis[c] = visible(c);
+                    for (int c = 0; c < 4; ++c) vis[c] = visible(c);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                v[32 * c + e] = ((vis[c] >> e) & 1u) ? v[32 * c + e] : __float_as_uint(-INFINITY);
-                    }
+                        for (int e = 0; e < 32; ++e)
+                            v[32 * c + e] = ((vis[c] >> e) & 1u) ? v[32 * c + e] : __float_as_uint(-INFINITY);
+                }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mx = fmaxf(mx, chunk_max<kMaskNone>(v + 32 * c, 0, 0, 0));
-                    new_reference();
-                    // P = 2^(s scale log2 e - m), written after the whole row was read (it may share S's columns)
-                    uint32_t pk[32];
+                for (int c = 0; c < 4; ++c) mx = fmaxf(mx, chunk_max<kMaskNone>(v + 32 * c, 0, 0, 0));
+                new_reference();
+                // P = 2^(s scale log2 e - m), written after the whole row was read (it may share S's columns)
+                uint32_t pk[32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        chunk_exp<kMaskNone>(v + 32 * c, 0, 0, 0, scale2, negm2, sum_a, sum_b, pk + 16 * (c & 1));
-                        if (c == 1) wait_pv();
-                        if (c & 1) {
-                            tmem_st16(tm_p + 16 * (c - 1), pk);
-                            tmem_st16(tm_p + 16 * c, pk + 16);
-                        }
-                    }
-                } else {
-                    // its 32-column chunks in loops, twice (maximum, then weights), those that no row of the warp
-                    // sees skipped
-                    auto scores = [&](int c, uint32_t vis, uint32_t (&v)[32]) {
-                        tmem_ld32(tm_s + 32 * c, v);
-                        tmem_wait_ld();
-                        regs_after_wait(v);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = ((vis >> e) & 1u) ? v[e] : __float_as_uint(-INFINITY);
-                    };
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t vis = visible(c);
-                        if (!__any_sync(0xffffffffu, vis != 0u)) continue;
-                        uint32_t v[32];
-                        scores(c, vis, v);
-                        mx = fmaxf(mx, chunk_max<kMaskNone>(v, 0, 0, 0));
-                    }
-                    new_reference();
-                    wait_pv();
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {  // (P's columns lie at or before those of scores already read)
-                        const uint32_t vis = visible(c);
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
-                        if (__any_sync(0xffffffffu, vis != 0u)) {
-                            uint32_t v[32];
-                            scores(c, vis, v);
-                            chunk_exp<kMaskNone>(v, 0, 0, 0, scale2, negm2, sum_a, sum_b, pk);
-                        }
-                        tmem_st16(tm_p + 16 * c, pk);
-                    }
-                    if (kSepP) {
-                        tc_fence_before();
-                        mbar_arrive(&bars->s_free[r]);
+                for (int c = 0; c < 4; ++c) {
+                    chunk_exp<kMaskNone>(v + 32 * c, 0, 0, 0, scale2, negm2, sum_a, sum_b, pk + 16 * (c & 1));
+                    if (c == 1) wait_pv();
+                    if (c & 1) {
+                        tmem_st16(tm_p + 16 * (c - 1), pk);
+                        tmem_st16(tm_p + 16 * c, pk + 16);
                     }
                 }
                 if (!ok) break;
@@ -873,11 +826,11 @@ __global__ void __launch_bounds__(256) attn_join_cuts_kernel(GatherProblem p, in
     }
 }
 
-template <int HD, bool PAGED, bool NARROW>
+template <int HD, bool PAGED>
 cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t stream) {
     constexpr int kSmem = TcLayout<HD>::kOffBar + kGBarBytes + 1024;  // + slack to align to 1024
-    cudaError_t e = cudaFuncSetAttribute(attn_gather_kernel<HD, PAGED, NARROW>,
+    cudaError_t e = cudaFuncSetAttribute(attn_gather_kernel<HD, PAGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int p_inv = (65536 + p.pack - 1) / p.pack;
@@ -891,7 +844,7 @@ cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_gather_kernel<HD, PAGED, NARROW>, tq, tk, tv, p, p_inv);
+    e = cudaLaunchKernelEx(&cfg, attn_gather_kernel<HD, PAGED>, tq, tk, tv, p, p_inv);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.n_cta, (p.tile_tokens * p.pack + 31) / 32);
     cfg.blockDim = dim3(256);
@@ -904,13 +857,9 @@ cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, cons
 cudaError_t launch_attn_gather(const GatherProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const CUtensorMap& tm_v, cudaStream_t stream) {
     if (p.head_dim != 64 && p.head_dim != 128) return cudaErrorInvalidValue;
-    const bool paged = p.kv_lens != nullptr, narrow = p.window > 0 && p.window <= kNarrowWindow;
-    auto* const launch =
-        p.head_dim == 128
-            ? (paged ? (narrow ? launch_gather_hd<128, true, true> : launch_gather_hd<128, true, false>)
-                     : (narrow ? launch_gather_hd<128, false, true> : launch_gather_hd<128, false, false>))
-            : (paged ? (narrow ? launch_gather_hd<64, true, true> : launch_gather_hd<64, true, false>)
-                     : (narrow ? launch_gather_hd<64, false, true> : launch_gather_hd<64, false, false>));
+    const bool paged = p.kv_lens != nullptr;
+    auto* const launch = p.head_dim == 128 ? (paged ? launch_gather_hd<128, true> : launch_gather_hd<128, false>)
+                                           : (paged ? launch_gather_hd<64, true> : launch_gather_hd<64, false>);
     return launch(p, tm_q, tm_k, tm_v, stream);
 }
 
