@@ -9,9 +9,9 @@
 // tile_tokens tokens. Packing the group multiplies the rows that each loaded key tile serves and lets
 // a few new tokens fill the M = 128 of the MMA. The key columns come in tiles of 128. Tiles of plain
 // window columns are fetched by TMA (documents: one box per 64 dimensions; pages: one per page piece).
-// A tile that holds sinks or ends the sequence is gathered row by row (cp.async with zero fill), so
-// the sinks share the tile of the window's end, and rows of no token, NaN in them included, never
-// meet a zero weight. Gathering every tile that way cost 5.2 us a tile against the 1.4 us of its
+// A tile that holds sinks or ends the sequence is gathered row by row (cp.async with zero fill; of
+// documents the whole groups of 8 window rows by TMA), so the sinks share the tile of the window's end,
+// and rows of no token, NaN in them included, never meet a zero weight. Gathering every tile that way cost 5.2 us a tile against the 1.4 us of its
 // products (3 warps issue 256 copies of 512 bytes and their addresses).
 //
 // CTA = 12 warps, one per SM, each with an equal share of all key tiles (gather_plan.cu):
@@ -22,7 +22,7 @@
 //               two sub-tiles (P V of the tile before, then S of this one). A whole warp with an elected
 //               lane for the MMAs, its index and branches uniform to the compiler, so that the MMAs'
 //               operands stay in uniform registers (under `if (lane == 0)`: 260 us instead of 205 for 4 x
-//               8192 tokens, 12 heads of 64, window 1024, 16 sinks; 324 instead of 304 for 2 x 8192, 32 / 8
+//               8192 tokens, 12 heads of 64, window 1024, 16 sinks; 324 instead of 306 for 2 x 8192, 32 / 8
 //               heads of 128)
 //   warps 9-11  loaders: plain key tiles by TMA (K: warp 9, V: warp 10, a lane per box), Q too where
 //               `pack` divides 128; gathered tiles and other Q by 16-byte cp.async into the same
@@ -44,6 +44,12 @@ namespace pha {
 namespace {
 
 constexpr int kLoadWarps = 3;
+
+// Bytes that the barrier's current phase awaits, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Register split: the softmax rows need all they can get (a spill in their loop goes to L2, the shared
 // memory leaves no L1 to speak of, and cost 1.6 times the time); 8 x 216 + 4 x 72 warps' shares use up
 // the launch's 12 x 168.
@@ -188,7 +194,8 @@ static_assert(sizeof(GBars) <= kGBarBytes, "barrier block");
 template <int HD, bool PAGED>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_gather_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const GatherProblem p, const int p_inv) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k8,
+                       const __grid_constant__ CUtensorMap tm_v8, const GatherProblem p, const int p_inv) {
     using L = TcLayout<HD>;
     constexpr bool kSepP = HD == 64;
     constexpr uint32_t kTmP = kSepP ? L::kTmO + 2 * HD : 0;
@@ -236,6 +243,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tma_prefetch_desc(&tm_q);
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
+            if (!PAGED) {
+                tma_prefetch_desc(&tm_k8);
+                tma_prefetch_desc(&tm_v8);
+            }
         }
         __syncwarp();
         tmem_alloc(&bars->tmem_base, L::kTmemCols);
@@ -271,20 +282,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto place = [&](uint32_t tile, int row) -> uint32_t {
             return tile + unit_off + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
         };
-        // The 128 rows of a K and a V tile whose pool rows are i0 .. i3 of lane row % 32 for the four blocks
-        // of 32 rows (negative: zeros). A small loop: unrolled, this code ran cold every time and took 5,000
-        // cycles a tile.
-        auto load_keys = [&](uint32_t k_tile, uint32_t v_tile, int i0, int i1, int i2, int i3, int head) {
+        // Rows [from, 128) of a K or V tile (`from` a multiple of 8) whose pool rows are i0 .. i3 of lane row % 32
+        // for the four blocks of 32 rows (negative: zeros). A small loop: unrolled, this code ran cold every
+        // time and took 5,000 cycles a tile.
+        auto load_rows = [&](uint32_t tile, const __nv_bfloat16* all, int from, int i0, int i1, int i2, int i3, int head) {
 #pragma unroll 2
-            for (int j = w; j < kBlockN / kRpi; j += kLoadWarps) {
+            for (int j = from / kRpi + w; j < kBlockN / kRpi; j += kLoadWarps) {
                 const int row = j * kRpi + row_in;
                 const int block = row >> 5;
                 const int mine = block == 0 ? i0 : (block == 1 ? i1 : (block == 2 ? i2 : i3));
                 const int x = __shfl_sync(0xffffffffu, mine, row & 31);
                 const int64_t at = (static_cast<int64_t>(x < 0 ? 0 : x) * p.kv_heads + head) * HD;
-                cp_async_16_zfill(place(k_tile, row), k_all + at, x < 0 ? 0u : 16u);
-                cp_async_16_zfill(place(v_tile, row), v_all + at, x < 0 ? 0u : 16u);
+                cp_async_16_zfill(place(tile, row), all + at, x < 0 ? 0u : 16u);
             }
+        };
+        // Documents: rows [0, 8 n) of a gathered tile, window columns all, by TMA in boxes of 8 rows, a lane per
+        // box; their bytes are awaited besides the loader threads' arrivals.
+        auto load_groups = [&](const CUtensorMap* map, int off, int64_t row0, int n, int head, uint64_t* bar) {
+            if (n == 0) return;
+            if (lane == 0) mbar_expect_tx(bar, n * 8 * HD * 2);
+            __syncwarp();
+            if (lane < n) {
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c)
+                    tma_load_2d(smem + off + c * L::kChunk + lane * 1024, map, head * HD + 64 * c,
+                                static_cast<int>(row0) + 8 * lane, bar);
+            }
+            __syncwarp();
         };
         // 128 consecutive columns by TMA, a lane per box; a page that is none reads as zeros (a row behind
         // the pool). Every loader thread arrives once per tile: here one of them with the bytes to come.
@@ -396,23 +420,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (w == 1) load_boxes(&tm_v, L::kOffV + sv * L::kKV, it, col0, head, &bars->v_full[sv]);
                     else mbar_arrive(&bars->v_full[sv]);
                 } else {
+                    // documents: whole groups of 8 window columns by TMA, the rest row by row. (Pages: the lookups in
+                    // between made it slower, 68 us instead of 63 for 24 sequences of 1 to 300 new tokens, 12 heads
+                    // of 64, window 1024; documents of 65,536 tokens, 6 paired heads of 128, window 128: 136 instead of 140; 2 x
+                    // 8192, 32 / 8 heads of 128, window 1024: 292 instead of 306.)
+                    const int plain = it.cols.n_w - col0 < kBlockN ? it.cols.n_w - col0 : kBlockN;
+                    const int groups = !PAGED && plain > 0 ? plain >> 3 : 0;
                     int idx[4];
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const int col = col0 + 32 * kk + lane;
                         idx[kk] = -1;
-                        if (col < it.cols.total) {
+                        if (col >= col0 + 8 * groups && col < it.cols.total) {
                             const int64_t row = key_row<PAGED>(p, it.where, it.where, col_pos(it.cols, col));
                             if (row < 0 && p.status) atomicMax(p.status, DEV_BAD_PAGE);
                             idx[kk] = static_cast<int>(row);
                         }
                     }
-                    ok = acquire(&bars->k_empty[sk], ((kc / L::kKStages) & 1) ^ 1) &&
-                         acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
+                    ok = acquire(&bars->k_empty[sk], ((kc / L::kKStages) & 1) ^ 1);
                     if (!ok) break;
-                    load_keys(sbase + L::kOffK + sk * L::kKV, sbase + L::kOffV + sv * L::kKV, idx[0], idx[1], idx[2],
-                              idx[3], head);
+                    if (!PAGED && w == 0)
+                        load_groups(&tm_k8, L::kOffK + sk * L::kKV, it.where + it.cols.lo + col0, groups, head, &bars->k_full[sk]);
+                    load_rows(sbase + L::kOffK + sk * L::kKV, k_all, 8 * groups, idx[0], idx[1], idx[2], idx[3], head);
                     cp_async_arrive(&bars->k_full[sk]);
+                    ok = acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
+                    if (!ok) break;
+                    if (!PAGED && w == 1)
+                        load_groups(&tm_v8, L::kOffV + sv * L::kKV, it.where + it.cols.lo + col0, groups, head, &bars->v_full[sv]);
+                    load_rows(sbase + L::kOffV + sv * L::kKV, v_all, 8 * groups, idx[0], idx[1], idx[2], idx[3], head);
                     cp_async_arrive(&bars->v_full[sv]);
                 }
                 // the second sub-tile's Q after the first key tile: its slot is free only when the previous
@@ -828,7 +863,8 @@ __global__ void __launch_bounds__(256) attn_join_cuts_kernel(GatherProblem p, in
 
 template <int HD, bool PAGED>
 cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                             const CUtensorMap& tv, cudaStream_t stream) {
+                             const CUtensorMap& tv, const CUtensorMap& tk8, const CUtensorMap& tv8,
+                             cudaStream_t stream) {
     constexpr int kSmem = TcLayout<HD>::kOffBar + kGBarBytes + 1024;  // + slack to align to 1024
     cudaError_t e = cudaFuncSetAttribute(attn_gather_kernel<HD, PAGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -844,7 +880,7 @@ cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_gather_kernel<HD, PAGED>, tq, tk, tv, p, p_inv);
+    e = cudaLaunchKernelEx(&cfg, attn_gather_kernel<HD, PAGED>, tq, tk, tv, tk8, tv8, p, p_inv);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.n_cta, (p.tile_tokens * p.pack + 31) / 32);
     cfg.blockDim = dim3(256);
@@ -855,12 +891,13 @@ cudaError_t launch_gather_hd(const GatherProblem& p, const CUtensorMap& tq, cons
 }  // namespace
 
 cudaError_t launch_attn_gather(const GatherProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                               const CUtensorMap& tm_v, cudaStream_t stream) {
+                               const CUtensorMap& tm_v, const CUtensorMap& tm_k8, const CUtensorMap& tm_v8,
+                               cudaStream_t stream) {
     if (p.head_dim != 64 && p.head_dim != 128) return cudaErrorInvalidValue;
     const bool paged = p.kv_lens != nullptr;
     auto* const launch = p.head_dim == 128 ? (paged ? launch_gather_hd<128, true> : launch_gather_hd<128, false>)
                                            : (paged ? launch_gather_hd<64, true> : launch_gather_hd<64, false>);
-    return launch(p, tm_q, tm_k, tm_v, stream);
+    return launch(p, tm_q, tm_k, tm_v, tm_k8, tm_v8, stream);
 }
 
 }  // namespace pha

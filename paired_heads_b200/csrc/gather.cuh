@@ -191,9 +191,11 @@ cudaError_t launch_gather_plan(const GatherProblem& p, int64_t max_tiles, int* b
                                bool strict, cudaStream_t stream);
 
 // bf16, head_dim 64 / 128, on the tensor cores, by the plan; then the cut items. tm_q: encode_pack_map
-// over q (used when pack divides 128); tm_k, tm_v: maps over the rows of k / v, 64 x box_rows boxes.
+// over q (used when pack divides 128); tm_k, tm_v: maps over the rows of k / v, 64 x box_rows boxes; tm_k8,
+// tm_v8: the same with boxes of 8 rows (documents; not used for pages).
 cudaError_t launch_attn_gather(const GatherProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                               const CUtensorMap& tm_v, cudaStream_t stream);
+                               const CUtensorMap& tm_v, const CUtensorMap& tm_k8, const CUtensorMap& tm_v8,
+                               cudaStream_t stream);
 
 // bf16, head_dim 64 / 128, few rows: at most kDecodeRows (new slots times a group's heads) a sequence, the
 // rows of its products; block per (split, kv head, sequence). (This and the row tiles of attn_gather.cu, us:

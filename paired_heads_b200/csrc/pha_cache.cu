@@ -386,7 +386,7 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
     if (launch_gather_plan(p, w.tiles, reinterpret_cast<int*>(base + w.space.before),
                            reinterpret_cast<int64_t*>(base + w.space.steps), false, stream) != cudaSuccess)
         return PHA_ERR_CUDA;
-    return of(launch_attn_gather(p, tq, tk, tv, stream));
+    return of(launch_attn_gather(p, tq, tk, tv, tk, tv, stream));
 }
 
 }  // extern "C"

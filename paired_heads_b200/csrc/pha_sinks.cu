@@ -160,13 +160,14 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
         return PHA_ERR_CUDA;
     if (!have || max_len == 0) return PHA_OK;
     if (!tc) return of(launch_attn_rows(p, stream));
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, tk8, tv8;
     const uint64_t rows = static_cast<uint64_t>(total_tokens) * p.mult;
     const uint64_t width = static_cast<uint64_t>(p.kv_heads) * head_dim;
     if (!encode_pack_map(&tq, q, head_dim, p.heads, rows, 128 % p.pack == 0 ? p.pack : 1) ||
-        !encode_slot_map(&tk, k, width, rows) || !encode_slot_map(&tv, v, width, rows))
+        !encode_slot_map(&tk, k, width, rows) || !encode_slot_map(&tv, v, width, rows) ||
+        !encode_slot_map(&tk8, k, width, rows, 8) || !encode_slot_map(&tv8, v, width, rows, 8))
         return PHA_ERR_CUDA;
-    return of(launch_attn_gather(p, tq, tk, tv, stream));
+    return of(launch_attn_gather(p, tq, tk, tv, tk8, tv8, stream));
 }
 
 pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const void* o,
