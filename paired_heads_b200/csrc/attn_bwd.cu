@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
         if (p.causal) {
             j1 = i + 1;
             if (p.window > 0 && i - p.window + 1 > j0) j0 = i - p.window + 1;
+            // with sinks: dS = P (dP - D) of a query that sees one key alone is 0, not the two sums' rounding
+            if (p.checked && j1 - j0 == 1 && (p.sinks == 0 || j0 == lo)) j1 = j0;
         }
     }
     if (threadIdx.x == 0) {
@@ -326,7 +328,8 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
                 }
                 group_sum2(s, dp);
                 const float pij = (i >= i0 && i < i1) ? exp2f(fmaf(s, scale2, -ls[ii])) : 0.f;
-                const float dsv = pij * (dp - dd[ii]) * p.scale;
+                const bool alone = p.checked && (i == lo || (p.window == 1 && p.sinks == 0));  // (as for dq)
+                const float dsv = alone ? 0.f : pij * (dp - dd[ii]) * p.scale;
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
                     axpy4(ak[t], dsv, qq[t]);

@@ -582,7 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     c_hi = slot - y_row;
                     c_sk = a + p.sinks - y_row;
                 }
-                if (!valid) c_hi = -1;
+                // (a query that sees one key alone has dS = P (dP - D) = 0 exactly; the two sums, taken in different
+                // orders, would leave 1e-7 where every gradient is zero)
+                if (!valid || (!KEYMAJOR && (slot == a || (window == 1 && p.sinks == 0)))) c_hi = -1;
                 // What nobody reads is left out: columns behind the sinks' slices in a step over them alone,
                 // rows that are no sinks in a far piece (their sums are not kept).
                 const bool idle = 64 * h >= n_cols || (KEYMAJOR && o.piece >= 0 && r0 >= p.sinks);
@@ -640,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     mbar_arrive(&bars->a_done);
                 }
+                if (KEYMAJOR && h == 0 && slot == a && y_row == a) pr[0] = 0.f;  // the document's first query, likewise
                 // stage B: dS = P (dP - D)
                 if (!wait(&bars->dp_full, g & 1)) break;
                 tc_fence_after();
@@ -730,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; store && w < (KEYMAJOR ? 2 : 1); ++w) {
                 // w = 0: the dS product (dQ or dK, times scale); w = 1: dV
                 const uint32_t col0 = L::kTmAcc + (KEYMAJOR && w == 0 ? HD : 0);
-                const float mul = w == 0 ? p.scale : 1.f;
+                // (window 1 without sinks: every query sees one key alone)
+                const float mul = w == 0 ? (window == 1 && p.sinks == 0 ? 0.f : p.scale) : 1.f;
                 uint4 w8[HD / 16];  // this half's columns of the row
 #pragma unroll
                 for (int cc = 0; cc < HD / 64; ++cc) {

@@ -319,3 +319,17 @@ def test_one_workspace_for_every_shape(pha):
             graphs[i].replay() if (turn + i) % 2 else step(i)
             for got, want in zip(outs[i], (wants[i][0], wants[i][1], *wants[i][2])):
                 assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("lens,window,sinks", [((1, 1, 1), 5, 2), ((1,), 0, 0), ((300, 1, 130), 1, 0), ((1, 1), 1, 3)])
+@pytest.mark.parametrize("dtype,H,Hkv,hd", [(BF16, 4, 2, 128), (BF16, 2, 2, 64), (F32, 4, 1, 48)])
+def test_queries_that_see_one_key_alone(pha, dtype, H, Hkv, hd, lens, window, sinks):
+    """Their softmax is 1 whatever q and k: dq and dk are zero, exactly, and dv the sum of dout."""
+    c = Case(lens, H, Hkv, hd, dtype, window, sinks, False, seed=7)
+    o, lse = c.forward(pha)
+    assert torch.equal(o.view(-1, Hkv, H // Hkv, hd), c.v[:, :, None].expand(-1, -1, H // Hkv, -1))
+    dq, dk, dv = c.backward(pha, o, lse)
+    assert not dq.any() and not dk.any()
+    want = c.dout.double().view(-1, Hkv, H // Hkv, hd).sum(2)
+    # P is 1 up to the rounding of the log-sum-exp (2^-22 of scores up to 2^6) and, in bf16, 1 itself
+    assert ((dv.double() - want).abs() <= torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -16 * want.abs().max()).all()
