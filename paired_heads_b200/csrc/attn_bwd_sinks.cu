@@ -802,42 +802,121 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, L::kTmemCols);
 }
 
-// -D_i = -dO_i . O_i and -lse_i log2(e) of every row (slot, head): 8 lanes per row, 16-byte loads. Reads
-// o and dout once (35 us for 65,536 tokens of 6 heads, hd 128: 5.8 TB/s) and uses no work list, so it runs
-// beside the lists' kernels (which take one CTA and 9 us each: 18 of 624 us for that step's training);
-// its last block waits for them, so that the grid's end is theirs too.
-template <int HD>
-__global__ void __launch_bounds__(256) attn_bwd_sinks_rows_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dout,
-                                                                  const float* __restrict__ lse, float* __restrict__ nlse,
-                                                                  float* __restrict__ nd, int64_t rows) {
-    const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t r = gid >> 3;
-    const int r8 = static_cast<int>(gid & 7);
+// Sum over the eight lanes of a row (in all of them); `group`: those lanes.
+__device__ __forceinline__ float row_sum(float x, uint32_t group) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) x += __shfl_xor_sync(group, x, s);
+    return x;
+}
+
+// This lane's part of the dot product of two rows of bf16.
+template <int N>
+__device__ __forceinline__ float row_dot(const uint4 (&a)[N], const uint4 (&b)[N]) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        const uint32_t x[4] = {a[t].x, a[t].y, a[t].z, a[t].w}, y[4] = {b[t].x, b[t].y, b[t].z, b[t].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            acc[w] = fmaf(__uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16),
+                          fmaf(__uint_as_float(x[w] & 0xFFFF0000u), __uint_as_float(y[w] & 0xFFFF0000u), acc[w]));
+    }
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
+// This lane's 16-byte units of row `row` of base [rows][HD].
+template <int HD>
+__device__ __forceinline__ void load_units(uint4 (&x)[HD / 64], const void* base, int64_t row) {
+#pragma unroll
+    for (int t = 0; t < HD / 64; ++t) x[t] = __ldg(static_cast<const uint4*>(base) + row * (HD / 8) + 8 * t + (threadIdx.x & 7));
+}
+
+// Rows that see few keys take D_i = sum_j P_ij dP_ij instead of dO_i . O_i, whose O is rounded to bf16: a
+// document's first kFewKeys rows (a document of 6 tokens: dq off by 8e-3 of its norm without, 2.45e-3 with),
+// and all rows where window and sinks are at most kFewWindow slots (window 6, 2 sinks: 2.6e-3 and 2.35e-3).
+// Beyond, that rounding is below the one of dS itself; so many rows of 16 keys would take 190 us of 390 (32,768
+// paired tokens of 6 heads of 128) for 2.5e-3 against 2.34e-3.
+constexpr int kFewKeys = 16, kFewWindow = 8;
+
+// The sum over the keys that the query of row r sees: its window's slots [win, slot] and the sinks before them,
+// from the document's start `from` on. dout: the row's units; group: the eight lanes of the row.
+template <int HD>
+__device__ __forceinline__ float few_keys_d(const AttnProblem& p, const uint4 (&dout)[HD / 64], int64_t r, int64_t slot,
+                                            int64_t from, float lse2, uint32_t group) {
+    const int64_t win = p.window > 0 && slot - from >= p.window ? slot - p.window + 1 : from;
+    const int n_sink = static_cast<int>(win - from < p.sinks ? win - from : p.sinks);
+    const int g = static_cast<int>(r - slot * p.heads) / (p.heads / p.kv_heads), n_win = static_cast<int>(slot - win) + 1;
+    uint4 q[HD / 64], k[HD / 64], v[HD / 64];
+    load_units<HD>(q, p.q, r);
+    float d = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < n_win + n_sink; ++j) {
+        const int64_t row = (j < n_win ? win + j : from + (j - n_win)) * p.kv_heads + g;
+        load_units<HD>(k, p.k, row);
+        load_units<HD>(v, p.v, row);
+        const float s = row_sum(row_dot(q, k), group), dp = row_sum(row_dot(dout, v), group);
+        d = fmaf(ex2(fmaf(s, p.scale * kLog2e, -lse2)), dp, d);
+    }
+    return d;
+}
+
+// -D_i and -lse_i log2(e) of every row (slot, head): 8 lanes per row, 16-byte loads. Reads o and dout once
+// (35 us for 65,536 tokens of 6 heads, hd 128: 5.8 TB/s) and uses no work list, so it runs beside the lists'
+// kernels (which take one CTA and 9 us each: 18 of 624 us for that step's training); its last block waits for
+// them, so that the grid's end is theirs too. FEW: no row sees more than kFewWindow keys; otherwise a document's
+// first rows have a kernel of their own (looking up every row's document here took 77 us). (cu_seqlens may be malformed here: what a row reads lies between its document's start and
+// itself.)
+template <int HD, bool FEW>
+__global__ void __launch_bounds__(256) attn_bwd_sinks_rows_kernel(const AttnProblem p, const uint4* __restrict__ o,
+                                                                  const uint4* __restrict__ dout, float* __restrict__ nlse,
+                                                                  float* __restrict__ nd, int64_t rows) {
+    if (!FEW) grid_dep_launch();
+    const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 3;
+    const uint32_t group = 0xFFu << (threadIdx.x & 24);
     if (r < rows) {
         uint4 a[HD / 64], b[HD / 64];
-#pragma unroll
-        for (int t = 0; t < HD / 64; ++t) {
-            a[t] = __ldg(o + r * (HD / 8) + 8 * t + r8);
-            b[t] = __ldg(dout + r * (HD / 8) + 8 * t + r8);
+        if (!FEW) load_units<HD>(a, o, r);
+        load_units<HD>(b, dout, r);
+        const float lse2 = p.lse[r] * kLog2e;
+        float d = 0.f;
+        if (!FEW) {
+            d = row_sum(row_dot(a, b), group);
+        } else {
+            const int64_t slot = static_cast<uint32_t>(r) / static_cast<uint32_t>(p.heads);
+            int doc = -1, z = p.batch;  // the last document that starts at or before the slot
+            while (z - doc > 1) {
+                const int mid = (doc + z) >> 1;
+                if (static_cast<int64_t>(__ldg(p.cu_seqlens + mid)) * p.slot_mult <= slot) doc = mid; else z = mid;
+            }
+            const int64_t from = doc < 0 ? -1 : static_cast<int64_t>(__ldg(p.cu_seqlens + doc)) * p.slot_mult;
+            if (from >= 0) d = few_keys_d<HD>(p, b, r, slot, from, lse2, group);
         }
-#pragma unroll
-        for (int t = 0; t < HD / 64; ++t) {
-            const uint32_t x[4] = {a[t].x, a[t].y, a[t].z, a[t].w}, y[4] = {b[t].x, b[t].y, b[t].z, b[t].w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                acc[w] = fmaf(__uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16),
-                              fmaf(__uint_as_float(x[w] & 0xFFFF0000u), __uint_as_float(y[w] & 0xFFFF0000u), acc[w]));
+        if ((threadIdx.x & 7) == 0) {
+            nd[r] = -d;
+            nlse[r] = -lse2;
         }
-    }
-    float d = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-#pragma unroll
-    for (int s = 1; s < 8; s <<= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-    if (r < rows && r8 == 0) {
-        nd[r] = -d;
-        nlse[r] = -lse[r] * kLog2e;
     }
     if (blockIdx.x == gridDim.x - 1) grid_dep_wait();
+}
+
+// -D of the first kFewKeys rows of every document, over what the kernel above (at the same time) writes there:
+// block (document, head).
+template <int HD>
+__global__ void __launch_bounds__(8 * kFewKeys) attn_bwd_sinks_starts_kernel(const AttnProblem p, const uint4* __restrict__ dout,
+                                                                             float* __restrict__ nd) {
+    const int64_t slots = static_cast<int64_t>(p.total_tokens) * p.slot_mult;
+    const int64_t from = static_cast<int64_t>(__ldg(p.cu_seqlens + blockIdx.x)) * p.slot_mult;
+    const int64_t to = static_cast<int64_t>(__ldg(p.cu_seqlens + blockIdx.x + 1)) * p.slot_mult;
+    const int64_t slot = from + (threadIdx.x >> 3), r = slot * p.heads + blockIdx.y;
+    const bool row = from >= 0 && slot < to && slot < slots;
+    float d = 0.f;
+    if (row) {
+        uint4 b[HD / 64];
+        load_units<HD>(b, dout, r);
+        d = few_keys_d<HD>(p, b, r, slot, from, p.lse[r] * kLog2e, 0xFFu << (threadIdx.x & 24));
+    }
+    grid_dep_wait();
+    if (row && (threadIdx.x & 7) == 0) nd[r] = -d;
 }
 
 // Block (document, kv head, 256 of the values): the sinks' rows of dk, dv of documents with far query
@@ -896,7 +975,6 @@ cudaError_t launch_attn_bwd_sinks_rows(const AttnProblem& p, const void* o, cons
     const int64_t rows = static_cast<int64_t>(p.total_tokens) * p.slot_mult * p.heads;
     const unsigned blocks = static_cast<unsigned>((rows * 8 + 255) / 256);
     const auto *a = static_cast<const uint4*>(o), *b = static_cast<const uint4*>(dout);
-    const float* lse = p.lse;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(256);
@@ -906,8 +984,16 @@ cudaError_t launch_attn_bwd_sinks_rows(const AttnProblem& p, const void* o, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return p.head_dim == 128 ? cudaLaunchKernelEx(&cfg, attn_bwd_sinks_rows_kernel<128>, a, b, lse, nlse, nd, rows)
-                             : cudaLaunchKernelEx(&cfg, attn_bwd_sinks_rows_kernel<64>, a, b, lse, nlse, nd, rows);
+    const bool few = p.window > 0 && p.window + p.sinks <= kFewWindow, wide = p.head_dim == 128;
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg,
+        wide ? (few ? attn_bwd_sinks_rows_kernel<128, true> : attn_bwd_sinks_rows_kernel<128, false>)
+             : (few ? attn_bwd_sinks_rows_kernel<64, true> : attn_bwd_sinks_rows_kernel<64, false>),
+        p, a, b, nlse, nd, rows);
+    if (e != cudaSuccess || few) return e;
+    cfg.gridDim = dim3(p.batch, p.heads);
+    cfg.blockDim = dim3(8 * kFewKeys);
+    return cudaLaunchKernelEx(&cfg, wide ? attn_bwd_sinks_starts_kernel<128> : attn_bwd_sinks_starts_kernel<64>, p, b, nd);
 }
 
 cudaError_t launch_attn_bwd_sinks_dq(const AttnProblem& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,

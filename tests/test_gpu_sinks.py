@@ -333,3 +333,22 @@ def test_queries_that_see_one_key_alone(pha, dtype, H, Hkv, hd, lens, window, si
     want = c.dout.double().view(-1, Hkv, H // Hkv, hd).sum(2)
     # P is 1 up to the rounding of the log-sum-exp (2^-22 of scores up to 2^6) and, in bf16, 1 itself
     assert ((dv.double() - want).abs() <= torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -16 * want.abs().max()).all()
+
+
+@pytest.mark.parametrize("lens,window,sinks,paired", [((6, 2, 3, 16, 17), 268, 33, False), ((2, 5), 3, 1, True),
+                                                      ((40, 700), 6, 2, False), ((700,), 7, 2, False),
+                                                      ((1000, 3), 90, 8, True)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_rows_with_few_keys_keep_the_precision(pha, hd, lens, window, sinks, paired):
+    """Norms of the errors of dq, dk: the results' rounding and that of dS, each uniform within half a
+    step (2^-8 of the value at most; a root mean square of 2^-8 / sqrt(3) is the most that gives), and as
+    much again for D and for the few rows of a short case: 2^-8 sqrt(3 / 3). Documents of a few tokens were
+    off by twice that with D from the rounded o."""
+    c = Case(lens, 4, 2, hd, BF16, window, sinks, paired, seed=11)
+    o, lse = c.forward(pha)
+    grads = c.backward(pha, o, lse)
+    ref = c.reference(grads=True)
+    check_grads(c, ref, grads)
+    want = [ref.dq.reshape(grads[0].shape), *(np.concatenate([x.reshape(-1, 2, hd) for x in y]) for y in (ref.dk, ref.dv))]
+    for got, w in zip(grads, want):
+        assert np.linalg.norm(f64(got) - w) <= 2.0 ** -8 * np.linalg.norm(w)
