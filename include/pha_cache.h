@@ -50,8 +50,9 @@ size_t pha_attn_paged_workspace_bytes(int batch, int max_q, int max_kv, int tota
  *   Query position p sees key position j iff j <= p and (window <= 0, or p - j < window, or
  *   j < sinks). window and sinks count key slots (on the paired path positions, lengths and pages
  *   double and heads halve, as in pha_attn_fwd). Pages no query sees are not read: their table
- *   entries may be -1 (pha_cache_trim). Rows behind a sequence's last token, of its last page too,
- *   are not read either, whatever they hold. Keys and values that are read must be finite.
+ *   entries may be -1 (pha_cache_trim). Keys and values of the positions that some query of the call
+ *   sees must be finite. Everything else in the pool may hold anything: rows behind a sequence's last
+ *   token, in its last page too, and rows between the sinks and its first query's window.
  *   max_q, max_kv: bounds of the new tokens and of kv_lens over the batch.
  *   Result: o = sum_j w_j v_j, w the softmax of scale * q.k_j over the visible keys; lse its
  *   logarithm of the sum of exponentials. scale <= 0 selects 1/sqrt(head_dim).

@@ -319,3 +319,39 @@ def test_long_cache_offsets_pass_32_bits(pha):
     ref = c.reference()
     o, lse = c.run(pha)
     ref.check(o, lse)
+
+
+WINDOWED = [c for c in CASES if c[7] and c[5] is BF16] + [
+    # chunks whose first column lies inside a box or a page, sinks below it and across it
+    ((300, 33), (1000, 815), 4, 2, 128, BF16, 64, 77, 0, False),
+    ((150,), (700,), 2, 2, 64, BF16, 32, 400, 148, False),                  # the sinks end in that box
+    ((150,), (700,), 2, 2, 64, BF16, 8, 531, 30, False),                    # the box begins with sinks
+    ((90, 90, 90, 90), (500, 501, 515, 531), 12, 4, 64, BF16, 16, 200, 3, False),
+    ((200,), (600,), 4, 4, 128, BF16, 256, 250, 5, True),
+]
+
+
+@pytest.mark.parametrize("case", WINDOWED, ids=str)
+def test_keys_that_no_query_sees_may_hold_anything(pha, case):
+    """NaN and infinities in keys and values between the sinks and the first query's window: they lie in
+    the boxes, pages and tiles of visible ones, and change no bit."""
+    c = Case(*case, seed=len(case[0]) + case[1][0])
+    ref = c.reference()
+    clean = c.run(pha)
+    mult, hkv = (2, c.Hkv // 2) if c.kw["paired"] else (1, c.Hkv)
+    page = c.k.shape[1] * mult
+    cu, table = c.cu.cpu().numpy(), c.table.cpu().numpy()
+    n = 0
+    for pool, bad in ((c.k, float("nan")), (c.v, float("inf"))):
+        rows = pool.view(-1, hkv, c.hd)
+        for b, kv in enumerate(c.lens.tolist()):
+            first = (kv - (cu[b + 1] - cu[b])) * mult
+            for j in range(c.kw["sinks"], max(first - c.kw["window"] + 1, 0)):
+                rows[table[b, j // page] * page + j % page] = bad if j % 3 else -bad
+                n += 1
+    assert n or max(case[1]) * mult <= c.kw["window"] + max(case[0]) * mult + c.kw["sinks"]
+    o, lse = c.run(pha)
+    ref.check(o, lse)
+    w = torch.from_numpy(ref.written.reshape(o.shape[0], -1).any(1))
+    assert torch.equal(o[w], clean[0][w]) and torch.equal(lse[w], clean[1][w])
+    assert c.status.item() == 0
