@@ -7,8 +7,12 @@
  * The cache. One layer's keys are k_pages[n_pages][page_size][n_kv_heads][head_dim], its values
  * v_pages likewise; page_size is a power of two. page_table[.][max_pages] (int32) has a row per
  * sequence: token p of sequence b lies in page page_table[b][p / page_size], row p % page_size.
- * Entries that hold no tokens are -1 (or anything: they are not read). On the paired path (pha.h)
- * a page's bytes are read as [2 * page_size][n_kv_heads / 2][head_dim], so the same cache serves it.
+ * A sequence without tokens (length 0) holds no pages, and its row may hold anything. In the row of
+ * one with tokens the entries behind its last page are -1, as pha_cache_reserve, _fork and _free leave
+ * them: pha_cache_fork and _free go by the whole row and take every entry that names a page for one
+ * that the sequence holds. (What no token lies in makes no difference to the other calls.) On the paired
+ * path (pha.h) a page's bytes are read as [2 * page_size][n_kv_heads / 2][head_dim], so the same cache
+ * serves it.
  * The calls that manage pages take all layers at once: k_cache[n_layers][n_pages][page_size]
  * [n_kv_heads][head_dim], v_cache likewise, and one page_table, kv_lens and page_refs for all of
  * them. page_refs[n_pages] (int32) counts the table entries that hold a page; 0 means free.
@@ -109,8 +113,9 @@ pha_status pha_cache_fork(int32_t* page_table, int max_pages, int32_t* kv_lens, 
 /*
  * pha_cache_reserve -- room for new_tokens[i] more tokens of sequence seqs[i] (each named once):
  *   kv_lens grows by them and the table gets the pages they need, lowest free page first, in the
- *   order of the list. A sequence that grows into a last page that it shares (page_refs > 1 before
- *   the call) gets a page of its own with the shared one's contents, in all layers, first.
+ *   order of the list (an empty sequence's row becomes -1 behind them). A sequence that grows into a
+ *   last page that it shares (page_refs > 1 before the call) gets a page of its own with the shared
+ *   one's contents, in all layers, first.
  *   page_bytes: bytes of one page of one layer and of K or V alone (page_size * n_kv_heads * head_dim
  *   * element size), a multiple of 16.
  *   Too few free pages: status 5; out of range, or longer than max_pages pages or 2^31 - 1 tokens:

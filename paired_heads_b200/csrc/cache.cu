@@ -122,7 +122,8 @@ __device__ int check_list(const CacheArgs& c, const int32_t* list, const int32_t
 }
 
 // Warp per sequence of the list, lanes over its table row. fork: dst takes over src's row and each
-// page gains a holder; otherwise (free) the sequence's pages lose one. Returns the entries handled.
+// page gains a holder; otherwise (free) the sequence's pages lose one. A sequence without tokens holds no
+// pages, whatever its row says. Returns the entries handled.
 template <bool FORK>
 __device__ int share_or_drop(const CacheArgs& c, const int32_t* src, const int32_t* list, int n,
                              int first_warp, int n_warps) {
@@ -131,15 +132,17 @@ __device__ int share_or_drop(const CacheArgs& c, const int32_t* src, const int32
     for (int i = first_warp; i < n; i += n_warps) {
         int32_t* to = c.table + static_cast<int64_t>(list[i]) * c.max_pages;
         const int32_t* from = FORK ? c.table + static_cast<int64_t>(src[i]) * c.max_pages : to;
+        const int len = c.lens[FORK ? src[i] : list[i]];
+        __syncwarp();  // (every lane has it before lane 0 writes the new one)
         for (int j = lane; j < c.max_pages; j += 32) {
-            const int page = from[j];
+            const int page = len > 0 ? from[j] : -1;
             if (page >= 0 && page < c.n_pages) {
                 atomicAdd(&c.refs[page], FORK ? 1 : -1);
                 ++count;
             }
             to[j] = FORK ? page : -1;
         }
-        if (lane == 0) c.lens[list[i]] = FORK ? c.lens[src[i]] : 0;
+        if (lane == 0) c.lens[list[i]] = FORK ? len : 0;
     }
     return count;
 }
@@ -251,11 +254,14 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(CacheArgs c, const in
         const int64_t len = c.lens[s];
         const int old = c.copy_src[i], need = c.need[i];
         const int64_t at = ((len + page_size - 1) >> page_shift) - (old >= 0 ? 1 : 0);
+        __syncwarp();  // (every lane has the length before lane 0 writes the new one)
         for (int j = lane; j < need; j += 32) {
             const int page = c.pages[c.first[i] + j];
             c.table[static_cast<int64_t>(s) * c.max_pages + at + j] = page;
             c.refs[page] = 1;
         }
+        if (len == 0 && need > 0)  // the row may hold anything so far; fork and free go by all of it
+            for (int64_t j = need + lane; j < c.max_pages; j += 32) c.table[static_cast<int64_t>(s) * c.max_pages + j] = -1;
         if (lane == 0) {
             c.copy_dst[i] = old >= 0 ? c.pages[c.first[i]] : -1;
             if (old >= 0) atomicSub(&c.refs[old], 1);

@@ -351,3 +351,46 @@ def test_reserving_past_31_bits_of_tokens(pha):
         pha.pha_cache_reserve(table, lens, refs, i32([0]), i32([new]), *pool, ws, status=status)
         assert status.item() == code and lens.item() == (1 << 31) - 1
         assert refs.tolist() == [0, 1, 0]
+
+
+@pytest.mark.parametrize("fill", ["zeros", "in range", "no page"])
+def test_tables_of_empty_sequences_may_hold_anything(pha, fill):
+    """A fresh table is not -1: the entries of a sequence without tokens name no pages. Reserve leaves -1
+    behind what it hands out, fork of and free of empty sequences touch no page."""
+    n_pages, page, n_seqs, max_pages = 30, 8, 7, 40
+    c = Cache(pha, n_pages, page, n_seqs, max_pages)
+    p = c.plain
+    rng = np.random.default_rng(1)
+    junk = {"zeros": np.zeros, "in range": lambda s: rng.integers(0, n_pages, s),
+            "no page": lambda s: rng.choice([-7, n_pages, 1 << 30], s)}[fill]((n_seqs, max_pages))
+    c.table.copy_(i32(junk))
+    touched = set()
+
+    def same():
+        rows = sorted(touched)
+        assert np.array_equal(c.table.cpu().numpy()[rows], p.table[rows])
+        assert np.array_equal(c.lens.cpu().numpy(), p.lens)
+        assert np.array_equal(c.refs.cpu().numpy(), p.refs)
+        assert np.array_equal(f64(c.k), p.k) and np.array_equal(f64(c.v), p.v)
+        assert c.status.item() == 0
+
+    def step(call, *lists, rows):
+        getattr(c, call)(*lists)
+        getattr(p, call)(*lists)
+        touched.update(rows)
+        same()
+
+    step("reserve", [0, 1], [20, 3], rows=[0, 1])
+    step("reserve", [2], [0], rows=[])                      # no tokens, no pages: still empty
+    assert c.count() == (0, 0)
+    step("free", [3], rows=[3])                             # never held anything
+    assert c.count() == (0, 0)
+    step("fork", [0, 4, 4], [5, 3, 6], rows=[5, 3, 6])      # of an empty one too
+    assert c.count() == (0, 3)
+    step("reserve", [3, 5], [9, 1], rows=[])
+    step("compact", rows=[])
+    step("free", [0, 5, 4], rows=[4])
+    step("reserve", [4, 0], [17, 1], rows=[])
+    step("compact", rows=[])
+    step("free", [0, 1, 3, 4, 6], rows=[])
+    assert not p.refs.any()
