@@ -165,9 +165,9 @@ __device__ __forceinline__ Tile decode_tile(int4 w, const AttnProblem& p, int G)
             lo = j;
             hi = last;
             if (p.window > 0) {
-                const int n_rows = min(kBlockM, b - o.row0);
-                const int q_last = o.row0 + n_rows - 1 + p.window - 1;
-                hi = (min(q_last, b - 1) - a) / kBlockN;
+                // (compared before they are added: the sum may pass 31 bits)
+                const int k_last = min(o.row0 + kBlockM, b) - 1;
+                hi = (k_last + min(p.window - 1, b - 1 - k_last) - a) / kBlockN;
             }
         }
         o.nq = hi - lo + 1;
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int c_lo, c_hi, c_sk = 0;
                 if (KEYMAJOR) {  // the queries that see key `slot`
                     c_lo = slot - y_row;
-                    c_hi = (window > 0 && slot - a >= p.sinks ? min(slot + window - 1, b - 1) : b - 1) - y_row;
+                    c_hi = (window > 0 && slot - a >= p.sinks ? slot + min(window - 1, b - 1 - slot) : b - 1) - y_row;
                 } else {         // the keys query `slot` sees
                     c_lo = (window > 0 ? max(a, slot - window + 1) : a) - y_row;
                     c_hi = slot - y_row;

@@ -31,6 +31,9 @@ pha_status shape_status(int batch, int max_len, int total_tokens, int n_heads, i
     return PHA_OK;
 }
 
+// No document is longer than the rows there are, however loose the bound max_len.
+int longest(int max_len, int total_tokens) { return max_len < total_tokens ? max_len : total_tokens; }
+
 // A window that reaches past the longest document hides nothing: no window (0), as the kernels' index
 // arithmetic wants it.
 int real_window(int window, int max_len, int paired) {
@@ -60,7 +63,8 @@ FwdPlan fwd_plan(int batch, int max_len, int n_heads, int n_kv_heads, int head_d
 
 // Backward: header, per-document scratch and work list of the query tiles, the same of the key tiles
 // (with far pieces; apart, so that a later call over the same documents keeps both lists), D (or -D),
-// -lse log2(e), the far pieces' partial sums.
+// -lse log2(e), the far pieces' partial sums. Every document's last tile and last piece may be ragged: at most
+// one of each more than whole ones fit.
 struct BwdPlan {
     int64_t items_q, items_k;
     size_t list, keys, dsum, nlse, part, bytes;  // list: of a work list behind its header
@@ -69,20 +73,25 @@ struct BwdPlan {
 BwdPlan bwd_plan(int batch, int max_len, int total_tokens, int n_heads, int n_kv_heads, int head_dim,
                  int window, int sinks, int paired) {
     const int mult = paired ? 2 : 1;
-    const int64_t tiles = (static_cast<int64_t>(max_len) * mult + kBlockN - 1) / kBlockN;
+    const int64_t slots = static_cast<int64_t>(total_tokens) * mult;
+    max_len = longest(max_len, total_tokens);
     window = real_window(window, max_len, paired);
     const bool far = window > 0 && sinks > 0;
     const int piece = far ? sink_piece_tiles(window, max_len, mult) : 1;
-    const int64_t pieces = far ? (tiles + piece - 1) / piece : 0;
+    // (documents of up to max_len, as long as the rows last)
+    const auto items = [&](int64_t rows) {
+        const int64_t each = (static_cast<int64_t>(max_len) * mult + rows - 1) / rows, all = slots / rows + batch;
+        return each > all / batch ? all : each * batch;
+    };
+    const int64_t tiles = items(kBlockN), pieces = far ? items(static_cast<int64_t>(piece) * kBlockN) : 0;
     BwdPlan w{};
-    w.items_q = static_cast<int64_t>(batch) * tiles * (n_heads / mult);
-    w.items_k = static_cast<int64_t>(batch) * (tiles + pieces) * (n_heads / mult);
+    w.items_q = tiles * (n_heads / mult);
+    w.items_k = (tiles + pieces) * (n_heads / mult);
     w.list = kWorkspaceHeaderBytes + workspace_doc_bytes(batch);
     w.keys = padded(w.list + sizeof(int4) * static_cast<size_t>(w.items_q));
     w.dsum = w.keys + padded(w.list + sizeof(int4) * static_cast<size_t>(w.items_k));
     w.nlse = w.dsum + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
     w.part = w.nlse + padded(sizeof(float) * static_cast<size_t>(total_tokens) * n_heads);
-    const int64_t slots = static_cast<int64_t>(total_tokens) * mult;
     w.bytes = w.part + (far ? padded(sizeof(float) * static_cast<size_t>(sink_part_slots(batch, slots, piece)) *
                                      (n_kv_heads / mult) * sinks * 2 * head_dim)
                             : 0);
@@ -140,7 +149,7 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
     p.heads = n_heads / p.mult;
     p.kv_heads = n_kv_heads / p.mult;
     p.head_dim = head_dim;
-    p.window = real_window(window, max_len, paired);
+    p.window = real_window(window, longest(max_len, total_tokens), paired);
     p.sinks = sinks;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     const FwdPlan w = fwd_plan(batch, max_len, n_heads, n_kv_heads, head_dim, window, sinks, paired);
@@ -196,14 +205,14 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
     p.v = v;
     p.cu_seqlens = cu_seqlens;
     p.batch = batch;
-    p.max_len = max_len;
+    p.max_len = longest(max_len, total_tokens);
     p.total_tokens = total_tokens;
     p.slot_mult = paired ? 2 : 1;
     p.heads = n_heads / p.slot_mult;
     p.kv_heads = n_kv_heads / p.slot_mult;
     p.head_dim = head_dim;
     p.causal = 1;
-    p.window = real_window(window, max_len, paired);
+    p.window = real_window(window, p.max_len, paired);
     p.sinks = p.window > 0 ? sinks : 0;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     p.lse = const_cast<float*>(lse);

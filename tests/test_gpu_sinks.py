@@ -352,3 +352,34 @@ def test_rows_with_few_keys_keep_the_precision(pha, hd, lens, window, sinks, pai
     want = [ref.dq.reshape(grads[0].shape), *(np.concatenate([x.reshape(-1, 2, hd) for x in y]) for y in (ref.dk, ref.dv))]
     for got, w in zip(grads, want):
         assert np.linalg.norm(f64(got) - w) <= 2.0 ** -8 * np.linalg.norm(w)
+
+
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (BF16, 128), (F32, 24)])
+@pytest.mark.parametrize("window,paired", [(2 ** 31 - 1, False), (2 ** 31 - 200, True), (2 ** 30 + 77, True),
+                                           (1400, True)])
+def test_loose_bounds_and_windows_past_everything(pha, dtype, hd, window, paired):
+    """max_len far above every document with a window below it: the window hides nothing, and no sum of a
+    position and the window wraps."""
+    c = Case((700,), 4, 2, hd, dtype, window, 3, paired, max_len=2 ** 31 - 1, tail=5)
+    o, lse = c.forward(pha)
+    assert pha.pha_attn_status(c.ws)[0] == 0
+    ref = c.reference(grads=True)
+    ref.check(o, lse)
+    check_grads(c, ref, c.backward(pha, o, lse))
+    assert pha.pha_attn_status(c.ws_bwd)[0] == 0
+    # the bits of a call without a window over a tight bound
+    tight = Case((700,), 4, 2, hd, dtype, 0, 0, paired, tail=5)
+    for a, b in zip(c.backward(pha, o, lse), tight.backward(pha, o, lse)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (F32, 16)])
+def test_many_documents_of_every_length(pha, dtype, hd):
+    """Lists and pieces at their bound: ragged tiles in every document, empty ones between."""
+    lens = [1, 0, 129, 257, 0, 1, 1, 385, 128, 127, 0, 1300, 1, 2, 3, 0, 1153] if dtype is BF16 else [1, 0, 33, 2, 0, 65, 1]
+    c = Case(lens, 2, 1, hd, dtype, 3, 2, False, max_len=10 ** 6)
+    o, lse = c.forward(pha)
+    ref = c.reference(grads=True)
+    ref.check(o, lse)
+    check_grads(c, ref, c.backward(pha, o, lse))
+    assert pha.pha_attn_status(c.ws_bwd)[0] == 0

@@ -226,3 +226,20 @@ def test_binding_checks_tensors(pha):
     with pytest.raises(TypeError, match="page_table"):
         pha.pha_cache_trim(torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, **i32),
                            torch.zeros(9, **i32), 16, window=4)
+
+
+def test_sinks_backward_workspace_follows_the_tokens(pha):
+    """A loose max_len costs nothing: no document is longer than all tokens."""
+    def size(batch, max_len, total, window=300, sinks=4, paired=False, H=8, Hkv=2, hd=128):
+        return pha.pha_attn_sinks_bwd_workspace_bytes(batch, max_len, total, H, Hkv, hd, window=window,
+                                                      sinks=sinks, paired=paired)
+
+    for paired in (False, True):
+        for total in (1, 127, 4096, 70000):
+            for batch in (1, 3, 200):
+                for window in (0, 1, 300, total, 2 ** 31 - 1):
+                    kw = dict(batch=batch, total=total, window=window, paired=paired)
+                    assert 0 < size(max_len=2 ** 31 - 1, **kw) == size(max_len=total, **kw) >= size(max_len=1, **kw)
+    # rows of total tokens and one ragged tile (and piece) a document, however many documents there are
+    per_item = 16 * 8
+    assert size(5000, 4096, 4096) <= size(1, 4096, 4096) + 5000 * (2 * per_item + per_item + 16 + 2 * 2 * 4 * 2 * 128 * 4) + 8192
