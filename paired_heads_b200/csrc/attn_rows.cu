@@ -33,6 +33,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(GatherProblem
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t rows = static_cast<int64_t>(p.total_q) * p.mult * p.heads;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
+    // the lengths of every sequence, those without a row of q too (documents: the plan has checked them)
+    if (PAGED && p.status && blockIdx.x == 0 && blockIdx.y == 0)
+        for (int b = threadIdx.x; b < p.batch; b += 32 * kRowWarps)
+            if (!gather_seq(p, b).ok) atomicMax(p.status, DEV_BAD_SEQLENS);
     if (row >= rows || (p.hdr && p.hdr->status != DEV_OK)) return;
     const int64_t slot = row / p.heads;
     const int h = static_cast<int>(row % p.heads), g = h / (p.heads / p.kv_heads);
@@ -40,11 +44,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(GatherProblem
     const int b = gather_seq_of(p.cu, p.batch, static_cast<int>(slot / p.mult));
     if (b < 0) return;
     const GatherSeq s = gather_seq(p, b);
-    if (!s.ok) {
-        if (p.status && lane == 0) atomicMax(p.status, DEV_BAD_SEQLENS);
-        return;
-    }
-    if (slot >= s.q0 + s.n_q) return;  // behind the last sequence
+    if (!s.ok || slot >= s.q0 + s.n_q) return;  // (behind the last sequence)
     // the columns of the whole sequence's queries when ranges are split (every split is of those)
     const int pos = s.kv - s.n_q + static_cast<int>(slot - s.q0);
     const GatherCols cols = gather_cols(p, pos, 1);

@@ -355,3 +355,52 @@ def test_keys_that_no_query_sees_may_hold_anything(pha, case):
     w = torch.from_numpy(ref.written.reshape(o.shape[0], -1).any(1))
     assert torch.equal(o[w], clean[0][w]) and torch.equal(lse[w], clean[1][w])
     assert c.status.item() == 0
+
+
+BAD_LENGTHS = [
+    # what is wrong with the first of three sequences of q new tokens over (300, 200, 64)
+    ("kv_lens", lambda c, q: c.lens.__setitem__(0, q - 1)),           # fewer than the new tokens
+    ("kv_lens", lambda c, q: c.lens.__setitem__(0, -5)),
+    ("kv_lens", lambda c, q: c.lens.__setitem__(0, 301)),             # beyond max_kv
+    ("kv_lens", lambda c, q: c.lens.__setitem__(0, 1 << 29)),
+    ("cu_seqlens", lambda c, q: c.cu.__setitem__(0, -1)),             # a row before q
+    ("max_q", lambda c, q: c.cu.copy_(torch.tensor([0, q + 1, 2 * q + 1, 3 * q + 1]))),
+]
+
+
+@pytest.mark.parametrize("q", [1, 3, 60])
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (F32, 16)])
+@pytest.mark.parametrize("bad", range(len(BAD_LENGTHS)))
+def test_a_bad_sequence_leaves_the_others_right(pha, dtype, hd, q, bad):
+    c = Case((q, q, q), (300, 200, 64), 4, 2, hd, dtype, 16, tail=1)
+    BAD_LENGTHS[bad][1](c, q)
+    lens = c.lens.clone()
+    c.lens.copy_(torch.tensor([300, 200, 64], dtype=torch.int32))
+    cu = c.cu.clone()
+    c.cu.clamp_(min=0)
+    ref = c.reference()                        # (of the others: the first one's rows are not looked at)
+    c.lens.copy_(lens)
+    c.cu.copy_(cu)
+    o, lse = c.run(pha)
+    assert c.status.item() == 1
+    cu = c.cu.tolist()
+    assert torch.isnan(o[:cu[1]]).all() and torch.isnan(lse[:cu[1]]).all()
+    ref.written[:cu[1]] = False
+    ref.check(o, lse)
+
+
+@pytest.mark.parametrize("q", [1, 2, 60])
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (F32, 16)])
+def test_sequences_wholly_outside_q_are_reported(pha, dtype, hd, q):
+    """Rows behind q and before it: status 1 whoever else is fine."""
+    for cu in ([0, q, 2 * q, 3 * q + 1], [0, q, 2 * q, 2 * q + 1], [-q, 0, q, 2 * q]):
+        c = Case((q, q, q), (300, 200, 64), 4, 2, hd, dtype, 16, max_q=q + 1)
+        c.q = c.q[:2 * q].contiguous()
+        good = [b for b in range(3) if cu[b] >= 0 and cu[b + 1] <= 2 * q]
+        c.cu.copy_(torch.tensor(cu))
+        o, lse = c.run(pha)
+        assert c.status.item() == 1, cu
+        whole = Case((q, q, q), (300, 200, 64), 4, 2, hd, dtype, 16, max_q=q + 1)
+        ref = Reference(f64(c.q), [cu[b] for b in good] + [cu[good[-1] + 1]], lambda i: whole.keys[good[i]][0],
+                        lambda i: whole.keys[good[i]][1], scale=c.scale, dtype=dtype, **c.kw)
+        ref.check(o, lse, cu)
