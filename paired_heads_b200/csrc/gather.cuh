@@ -160,7 +160,7 @@ inline int gather_tile_tokens(int pack, int window, int sinks, int align) {
 inline int64_t gather_tiles(int batch, int64_t max_q, int64_t total_q, int tile_tokens) {
     const int64_t per_seq = (max_q + tile_tokens - 1) / tile_tokens;
     const int64_t by_rows = total_q / tile_tokens + batch;
-    return per_seq * batch < by_rows ? per_seq * batch : by_rows;
+    return per_seq > by_rows / batch ? by_rows : per_seq * batch;  // (their product may pass 63 bits)
 }
 
 constexpr int kGatherCtas = 148;      // SMs of a B200; workspaces may not depend on the device at hand

@@ -367,7 +367,6 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
         if (e == cudaSuccess && p.n_splits > 1) e = launch_attn_join(p, w.decode, stream);
         return of(e);
     }
-    if (max_q == 0) return PHA_OK;
     p.hdr = reinterpret_cast<WorkspaceHeader*>(base);
     p.tiles = reinterpret_cast<int4*>(base + w.space.tiles);
     p.starts = reinterpret_cast<int4*>(base + w.space.starts);
@@ -386,6 +385,7 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
     if (launch_gather_plan(p, w.tiles, reinterpret_cast<int*>(base + w.space.before),
                            reinterpret_cast<int64_t*>(base + w.space.steps), false, stream) != cudaSuccess)
         return PHA_ERR_CUDA;
+    if (w.tiles == 0) return PHA_OK;  // no new tokens are allowed for: the plan has checked the lengths
     return of(launch_attn_gather(p, tq, tk, tv, tk, tv, stream));
 }
 

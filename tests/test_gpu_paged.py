@@ -404,3 +404,18 @@ def test_sequences_wholly_outside_q_are_reported(pha, dtype, hd, q):
         ref = Reference(f64(c.q), [cu[b] for b in good] + [cu[good[-1] + 1]], lambda i: whole.keys[good[i]][0],
                         lambda i: whole.keys[good[i]][1], scale=c.scale, dtype=dtype, **c.kw)
         ref.check(o, lse, cu)
+
+
+@pytest.mark.parametrize("dtype,hd,q", [(BF16, 64, 1), (F32, 8, 1)])
+def test_more_sequences_than_a_grid_has_columns(pha, dtype, hd, q):
+    """70,000 sequences; then a call that allows no new tokens where a sequence has some."""
+    n = 70000
+    c = Case((q,) * 3 + (0,) * (n - 6) + (q,) * 3, (40, 3, 17) + (0,) * (n - 6) + (1, 9, 33), 2, 1, hd, dtype, 16)
+    ref = c.reference()
+    o, lse = c.run(pha)
+    ref.check(o, lse)
+    assert c.status.item() == 0
+    c.max_q = 0
+    o, lse = c.run(pha)
+    assert c.status.item() == 1
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
