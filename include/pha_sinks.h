@@ -28,7 +28,8 @@ size_t pha_attn_sinks_bwd_workspace_bytes(int batch, int max_len, int total_toke
  *   supported types (bf16 with head_dim 64 / 128; f32 with head_dim 1 .. 128), device status
  *   (pha_attn_status(workspace)) and errors as pha_attn_fwd with causal = 1, and:
  *   sinks: 0 <= sinks, else PHA_ERR_INVALID; more than 128: PHA_ERR_UNSUPPORTED.
- *   total_tokens * n_heads beyond 2^31 - 1 rows: PHA_ERR_INVALID.
+ *   total_tokens * n_heads beyond 2^31 - 1 rows, batch * min(max_len, 2^29) beyond 2^48:
+ *   PHA_ERR_INVALID.
  *   workspace: pha_attn_sinks_workspace_bytes(...) bytes, needed for f32 too. Rows outside every
  *   document are not written. k and v rows inside the documents must be finite.
  */

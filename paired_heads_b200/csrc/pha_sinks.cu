@@ -17,12 +17,16 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 pha_status of(cudaError_t e) { return e == cudaSuccess ? PHA_OK : PHA_ERR_CUDA; }
 
-// Shape checks of both directions.
+constexpr int kMostTokens = 1 << 29;
+
+// Shape checks of both directions. (batch times the longest document is bounded so that workspace sizes, which
+// grow with it, fit 64 bits.)
 pha_status shape_status(int batch, int max_len, int total_tokens, int n_heads, int n_kv_heads,
                         int head_dim, pha_dtype dtype, int sinks, int paired, float scale) {
     if ((dtype != PHA_BF16 && dtype != PHA_F32) || batch <= 0 || max_len < 0 || total_tokens < 0 ||
-        total_tokens > (1 << 29) || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
+        total_tokens > kMostTokens || n_heads <= 0 || n_kv_heads <= 0 || n_heads > 4096 ||
         static_cast<int64_t>(total_tokens) * n_heads > INT32_MAX ||
+        static_cast<int64_t>(batch) * (max_len < kMostTokens ? max_len : kMostTokens) > static_cast<int64_t>(1) << 48 ||
         n_heads % n_kv_heads != 0 || head_dim <= 0 || sinks < 0 || (paired != 0 && paired != 1) ||
         !(scale == scale) || (paired && ((n_heads & 1) || (n_kv_heads & 1))))
         return PHA_ERR_INVALID;
@@ -52,6 +56,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(int batch, int max_len, int n_heads, int n_kv_heads, int head_dim, int window, int sinks,
                  int paired) {
     const int mult = paired ? 2 : 1;
+    max_len = longest(max_len, kMostTokens);
     const int64_t slots = static_cast<int64_t>(max_len) * mult;
     FwdPlan w;
     w.pack = gather_pack(n_heads / mult, n_kv_heads / mult);

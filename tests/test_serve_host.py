@@ -243,3 +243,21 @@ def test_sinks_backward_workspace_follows_the_tokens(pha):
     # rows of total tokens and one ragged tile (and piece) a document, however many documents there are
     per_item = 16 * 8
     assert size(5000, 4096, 4096) <= size(1, 4096, 4096) + 5000 * (2 * per_item + per_item + 16 + 2 * 2 * 4 * 2 * 128 * 4) + 8192
+
+
+def test_sinks_workspace_bytes_never_wrap(pha):
+    """Bounds of batch and max_len whose workspace would not fit 64 bits are invalid arguments; below, the size
+    covers 24 bytes for each row tile that a batch of longest documents has."""
+    for H, Hkv, paired in ((256, 2, True), (2, 2, False), (34, 2, False)):
+        pack = H // Hkv
+        for batch in (1, 1000, 1 << 19, 1 << 20, 1 << 29, 2 ** 31 - 1):
+            for max_len in (1, 5000, 1 << 28, 1 << 29, 2 ** 31 - 1):
+                size = pha.pha_attn_sinks_workspace_bytes(batch, max_len, H, Hkv, 64, window=0, sinks=4,
+                                                          paired=paired)
+                length = min(max_len, 1 << 29)         # total_tokens is at most that
+                if batch * length > 1 << 48:
+                    assert size == 0, (batch, max_len)
+                    assert _sinks(pha, batch=batch, max_len=max_len, H=H, Hkv=Hkv, paired=int(paired), bytes=2 ** 63) == -1
+                else:
+                    tiles = batch * -(-length * (2 if paired else 1) // (256 // pack))
+                    assert size >= 24 * tiles, (batch, max_len)
