@@ -471,9 +471,20 @@ def _nbytes(t) -> int:
     return t.nbytes
 
 
+_MOST = 2 ** 31
+
+
+def _cut(*counts):
+    """Counts of slots within the C side's 32 bits. ctypes would wrap them without a word (a window of 2^32 + 5
+    would be one of 5); the nearest count that fits means the same or is refused by the library."""
+    return [max(-_MOST, min(x, _MOST - 1)) for x in counts]
+
+
 def pha_attn_sinks_workspace_bytes(batch: int, max_len: int, n_heads: int, n_kv_heads: int,
                                    head_dim: int, *, window: int, sinks: int,
                                    paired: bool = False) -> int:
+    if not (-_MOST <= window < _MOST and -_MOST <= sinks < _MOST):
+        window, sinks = _cut(window, sinks)
     return int(_lib.pha_attn_sinks_workspace_bytes(batch, max_len, n_heads, n_kv_heads, head_dim,
                                                    window, sinks, int(paired)))
 
@@ -481,6 +492,8 @@ def pha_attn_sinks_workspace_bytes(batch: int, max_len: int, n_heads: int, n_kv_
 def pha_attn_sinks_bwd_workspace_bytes(batch: int, max_len: int, total_tokens: int, n_heads: int,
                                        n_kv_heads: int, head_dim: int, *, window: int, sinks: int,
                                        paired: bool = False) -> int:
+    if not (-_MOST <= window < _MOST and -_MOST <= sinks < _MOST):
+        window, sinks = _cut(window, sinks)
     return int(_lib.pha_attn_sinks_bwd_workspace_bytes(batch, max_len, total_tokens, n_heads,
                                                        n_kv_heads, head_dim, window, sinks,
                                                        int(paired)))
@@ -490,6 +503,8 @@ def pha_attn_sinks_fwd(q, k, v, cu_seqlens, max_len: int, o, lse, workspace, *, 
                        sinks: int, paired: bool = False, scale: float = 0.0, stream=None):
     """Causal varlen attention with a sliding window and `sinks` visible first slots per document,
     into o (like q) and lse [T][H] float32 (or None). pha_attn_status(workspace) reports."""
+    if not (-_MOST <= window < _MOST and -_MOST <= sinks < _MOST):
+        window, sinks = _cut(window, sinks)
     t, h, hkv, hd, dt, code = _dims(q, k)
     n = cu_seqlens.shape[0]
     _run("pha_attn_sinks_fwd",
@@ -505,6 +520,8 @@ def pha_attn_sinks_bwd(q, k, v, o, lse, dout, cu_seqlens, max_len: int, dq, dk, 
                        window: int, sinks: int, paired: bool = False, scale: float = 0.0,
                        stream=None):
     """Backward of pha_attn_sinks_fwd (o, lse: its outputs): dq, dk, dv for dout."""
+    if not (-_MOST <= window < _MOST and -_MOST <= sinks < _MOST):
+        window, sinks = _cut(window, sinks)
     t, h, hkv, hd, dt, code = _dims(q, k)
     n = cu_seqlens.shape[0]
     like_q, like_k = (t, h, hd), (t, hkv, hd)
@@ -523,6 +540,8 @@ def pha_attn_paged_workspace_bytes(batch: int, max_q: int, max_kv: int, total_q:
                                    n_kv_heads: int, head_dim: int, dtype, *, window: int = 0,
                                    sinks: int = 0, paired: bool = False) -> int:
     """dtype: torch.bfloat16 or torch.float32."""
+    if not (-_MOST <= window < _MOST and -_MOST <= sinks < _MOST):
+        window, sinks = _cut(window, sinks)
     import torch
 
     code = PHA_BF16 if dtype == torch.bfloat16 else PHA_F32
@@ -537,6 +556,8 @@ def pha_attn_paged_fwd(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, max
     """Attention of each sequence's new tokens q over its paged cache (k_pages, v_pages
     [pages][page_size][Hkv][hd], page_table [batch][max_pages], kv_lens [batch] with the new tokens
     included) into o and lse (or None). status: int32[1], raised on bad lengths or pages."""
+    if not (-_MOST <= window < _MOST and -_MOST <= sinks < _MOST):
+        window, sinks = _cut(window, sinks)
     t, h, hkv, hd, dt, code = _dims(q, k_pages)
     pool = k_pages.shape
     n_pages, page = pool[0], pool[1]
@@ -638,6 +659,7 @@ def pha_cache_free(page_table, kv_lens, page_refs, seqs, workspace, *, status=No
 def pha_cache_trim(page_table, kv_lens, page_refs, page_size: int, *, window: int, sinks: int = 0,
                    paired: bool = False, status=None, stream=None):
     """Every sequence lets go of the pages that no later token sees with this window and sinks."""
+    window, sinks, page_size = _cut(window, sinks, page_size)
     wanted, mp, ns, npg = _cache_tensors(page_table, kv_lens, page_refs, status)
     _run("pha_cache_trim", wanted,
          (page_table.data_ptr(), mp, kv_lens.data_ptr(), ns, page_refs.data_ptr(), npg, page_size,

@@ -261,3 +261,39 @@ def test_sinks_workspace_bytes_never_wrap(pha):
                 else:
                     tiles = batch * -(-length * (2 if paired else 1) // (256 // pack))
                     assert size >= 24 * tiles, (batch, max_len)
+
+
+def test_windows_past_32_bits_do_not_wrap(pha, monkeypatch):
+    """The library is called with the nearest count that fits: a window of 2^32 + 5 hides nothing (no more than
+    one of 2^31 - 1) and is not one of 5, and sinks of 2^32 + 4 are not 4."""
+    import torch
+
+    seen = []
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(1 << 12, dtype=torch.uint8)
+    i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32)
+    pool = torch.zeros(3, 4, 2, 64, dtype=torch.bfloat16)
+    lse = torch.zeros(4, 2)
+    calls = {
+        "pha_attn_sinks_fwd": (11, lambda **kw: pha.pha_attn_sinks_fwd(q, q, q, i32(2), 4, q, None, ws, **kw)),
+        "pha_attn_sinks_bwd": (14, lambda **kw: pha.pha_attn_sinks_bwd(q, q, q, q, lse, q, i32(2), 4, q, q, q, ws, **kw)),
+        "pha_attn_paged_fwd": (17, lambda **kw: pha.pha_attn_paged_fwd(
+            q, pool, pool, i32(1, 3), i32(2), i32(1), 4, 9, q, None, ws, **kw)),
+        "pha_cache_trim": (7, lambda **kw: pha.pha_cache_trim(i32(2, 3), i32(2), i32(9), 16, **kw)),
+    }
+    monkeypatch.setattr(pha, "_run", lambda fn, wanted, args, stream: seen.append((fn, args)))
+    top, low = 2 ** 31 - 1, -2 ** 31
+    for given, wanted in ((2 ** 31, top), (2 ** 32 + 5, top), (2 ** 63, top), (low - 1, low), (-2 ** 40, low),
+                          (top, top), (77, 77), (-1, -1)):
+        for fn, (at, call) in calls.items():
+            call(window=given, sinks=3)
+            call(window=9, sinks=given)
+            (name, a), (_, b) = seen[-2:]
+            assert name == fn and a[at:at + 2] == (wanted, 3) and b[at:at + 2] == (9, wanted), (fn, given)
+    pha.pha_cache_trim(i32(2, 3), i32(2), i32(9), 2 ** 32 + 16, window=5)
+    assert seen[-1][1][6] == top                       # (no power of two: refused)
+    size = lambda w, s: (pha.pha_attn_sinks_workspace_bytes(1, 900, 2, 2, 64, window=w, sinks=s),
+                         pha.pha_attn_sinks_bwd_workspace_bytes(1, 900, 900, 2, 2, 64, window=w, sinks=s),
+                         pha.pha_attn_paged_workspace_bytes(1, 1, 90000, 1, 2, 2, 64, torch.bfloat16, window=w, sinks=s))
+    assert size(2 ** 32 + 5, 1) == size(0, 1) != size(5, 1)
+    assert size(5, 2 ** 32 + 4)[:2] == (0, 0) and size(5, 2 ** 32 + 4)[2] == size(0, 0)[2]
