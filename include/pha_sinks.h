@@ -42,7 +42,9 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
 /*
  * pha_attn_sinks_bwd -- dq, dk, dv of pha_attn_sinks_fwd for the upstream gradient dout; arguments,
  *   arithmetic and errors as pha_attn_bwd with the mask above. o, lse: the forward's outputs. Rows
- *   outside every document get zeros. No atomics: the same inputs give the same bits.
+ *   outside every document get zeros. No atomics: the same inputs give the same bits. Malformed
+ *   cu_seqlens: status 1 (pha_attn_status(workspace)); no gradient is computed, rows outside
+ *   [cu_seqlens[0], cu_seqlens[batch]) may get their zeros all the same.
  */
 pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const void* o,
                               const float* lse, const void* dout, const int32_t* cu_seqlens,

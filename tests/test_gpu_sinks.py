@@ -383,3 +383,63 @@ def test_many_documents_of_every_length(pha, dtype, hd):
     ref.check(o, lse)
     check_grads(c, ref, c.backward(pha, o, lse))
     assert pha.pha_attn_status(c.ws_bwd)[0] == 0
+
+
+MALFORMED = [[0, 120, 100], [-1, 100, 160], [0, 100, 161], [0, 10, 160],          # (the last: too long)
+             [170, 170, 170], [0, -3, 160], [-5, -4, -3], [2 ** 31 - 1, 0, 160], [0, 2 ** 31 - 1, -2 ** 31],
+             [40, 100, 130]]                                                        # well formed, rows around it
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,hd,window,sinks,paired", [
+    (BF16, 2, 2, 64, 16, 2, False), (BF16, 4, 2, 128, 16, 2, True), (BF16, 4, 2, 64, 5, 2, False),   # (5 + 2: D from keys)
+    (BF16, 2, 2, 128, 7, 0, True), (BF16, 2, 1, 64, 0, 3, False), (F32, 4, 2, 24, 9, 3, False), (F32, 2, 2, 16, 0, 0, True)])
+def test_malformed_documents_in_both_directions(pha, dtype, H, Hkv, hd, window, sinks, paired):
+    """Status 1, nothing written forward, and no gradient row other than zeros outside [cu[0], cu[-1]); the same
+    workspaces then serve well-formed documents."""
+    c = Case((100, 60), H, Hkv, hd, dtype, window, sinks, paired, max_len=130)
+    good = c.cu.clone()
+    o, lse = c.forward(pha)
+    want = c.backward(pha, o, lse)
+    ws, n = c.ws_bwd, c.q.shape[0]
+    for bad in MALFORMED:
+        ok = bad == MALFORMED[-1]
+        c.cu.copy_(torch.tensor(bad, dtype=torch.int32))
+        got, got_lse = c.forward(pha, ws=c.ws)
+        assert pha.pha_attn_status(c.ws)[0] == (0 if ok else 1), bad
+        if not ok:
+            assert torch.isnan(got).all() and torch.isnan(got_lse).all(), bad
+        grads = [torch.full_like(x, float("nan")) for x in want]
+        pha.pha_attn_sinks_bwd(c.q, c.k, c.v, o, lse, c.dout, c.cu, c.max_len, *grads, ws, **c.kw)
+        assert pha.pha_attn_status(ws)[0] == (0 if ok else 1), bad
+        lo, hi = max(min(bad[0], n), 0), max(min(bad[2], n), 0)
+        for g in grads:
+            inside = g[lo:max(hi, lo)]
+            assert ok or torch.isnan(inside).all(), bad
+            assert (torch.isnan(g) | (g == 0)).all() or ok, bad
+            if ok:
+                assert torch.isfinite(g).all() and not g[:lo].any() and not g[hi:].any()
+        c.cu.copy_(good)
+        grads = [torch.full_like(x, float("nan")) for x in want]
+        pha.pha_attn_sinks_bwd(c.q, c.k, c.v, o, lse, c.dout, c.cu, c.max_len, *grads, ws, **c.kw)
+        for a, b in zip(grads, want):
+            assert torch.equal(a, b), bad
+
+
+def test_malformed_documents_with_far_pieces(pha):
+    """Sinks that many query tiles see: the pieces' sums are not taken either."""
+    c = Case((4100, 1500), 2, 2, 64, BF16, 60, 4, False, max_len=4200)
+    o, lse = c.forward(pha)
+    want = c.backward(pha, o, lse)
+    good = c.cu.clone()
+    for bad in ([0, 4300, 5600], [0, 4100, 5601], [-1, 4099, 5600], [0, 4100, 4000]):
+        c.cu.copy_(torch.tensor(bad, dtype=torch.int32))
+        grads = [torch.full_like(x, float("nan")) for x in want]
+        pha.pha_attn_sinks_bwd(c.q, c.k, c.v, o, lse, c.dout, c.cu, c.max_len, *grads, c.ws_bwd, **c.kw)
+        assert pha.pha_attn_status(c.ws_bwd)[0] == 1, bad
+        for g in grads:
+            assert torch.isnan(g[:min(bad[2], 5600)]).all() and not g[min(bad[2], 5600):].any(), bad
+    c.cu.copy_(good)
+    grads = [torch.full_like(x, float("nan")) for x in want]
+    pha.pha_attn_sinks_bwd(c.q, c.k, c.v, o, lse, c.dout, c.cu, c.max_len, *grads, c.ws_bwd, **c.kw)
+    for a, b in zip(grads, want):
+        assert torch.equal(a, b)
