@@ -81,6 +81,24 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
                               size_t workspace_bytes, int32_t* status, pha_stream_t stream);
 
 /*
+ * pha_test_attn_paged_fwd_stalled -- failure-detection test hook; not for production use.
+ *   pha_attn_paged_fwd (same arguments, same checks) whose softmax warps first wait up to stall_us
+ *   microseconds on a barrier that nothing signals: status 3, every role winds down, no row of o or
+ *   lse is written. The GPU context and the workspace stay usable, as with
+ *   pha_test_attn_fwd_stalled. stall_us: 1 .. 100000, else PHA_ERR_INVALID; f32 and calls of few rows
+ *   a sequence (bf16, max_q times the heads of a group at most 16) have no waits: PHA_ERR_UNSUPPORTED.
+ */
+pha_status pha_test_attn_paged_fwd_stalled(const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, int max_pages, int n_pages,
+                                           int page_size, const int32_t* cu_seqlens,
+                                           const int32_t* kv_lens, int batch, int max_q, int max_kv,
+                                           int total_q, int n_heads, int n_kv_heads, int head_dim,
+                                           pha_dtype dtype, int window, int sinks, int paired,
+                                           float scale, void* o, float* lse, void* workspace,
+                                           size_t workspace_bytes, int32_t* status, int stall_us,
+                                           pha_stream_t stream);
+
+/*
  * pha_cache_append -- writes the new tokens' keys and values (rotated already: pha_rope) to their
  *   places in one layer's pages. k, v: [total][n_kv_heads][head_dim]; cu_seqlens, kv_lens (new
  *   tokens included), page_table as pha_attn_paged_fwd. Any type: element_bytes is 1, 2 or 4, and

@@ -53,6 +53,31 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
                               int paired, float scale, void* dq, void* dk, void* dv,
                               void* workspace, size_t workspace_bytes, pha_stream_t stream);
 
+/*
+ * pha_test_attn_sinks_fwd_stalled, pha_test_attn_sinks_bwd_stalled -- failure-detection test hooks; not
+ *   for production use. The call of the same name without test_ and _stalled (same arguments, same
+ *   checks), whose softmax (elementwise) warps first wait up to stall_us microseconds on a barrier
+ *   that nothing signals: device status 3, every role winds down, and no row of o, lse, dq, dk or dv
+ *   inside a document is written. The GPU context and the workspace stay usable, as with
+ *   pha_test_attn_fwd_stalled. stall_us: 1 .. 100000, else PHA_ERR_INVALID; PHA_F32 has no waits:
+ *   PHA_ERR_UNSUPPORTED.
+ */
+pha_status pha_test_attn_sinks_fwd_stalled(const void* q, const void* k, const void* v,
+                                           const int32_t* cu_seqlens, int batch, int max_len,
+                                           int total_tokens, int n_heads, int n_kv_heads,
+                                           int head_dim, pha_dtype dtype, int window, int sinks,
+                                           int paired, float scale, void* o, float* lse,
+                                           void* workspace, size_t workspace_bytes, int stall_us,
+                                           pha_stream_t stream);
+pha_status pha_test_attn_sinks_bwd_stalled(const void* q, const void* k, const void* v,
+                                           const void* o, const float* lse, const void* dout,
+                                           const int32_t* cu_seqlens, int batch, int max_len,
+                                           int total_tokens, int n_heads, int n_kv_heads,
+                                           int head_dim, pha_dtype dtype, int window, int sinks,
+                                           int paired, float scale, void* dq, void* dk, void* dv,
+                                           void* workspace, size_t workspace_bytes, int stall_us,
+                                           pha_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

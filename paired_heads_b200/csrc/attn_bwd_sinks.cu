@@ -114,6 +114,7 @@ struct Bars {
     uint64_t m2_done[2];        // key-major: dV's / dK's product complete (P's / dS's columns are free);
                                 // query-major: dQ's of dS buffer i
     uint64_t acc_full, acc_empty, drain[2];
+    uint64_t stall;             // never signalled: the failure-detection test hook waits on it
     uint32_t tmem_base;
     int abort;
     StepRec step[3];
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars->acc_empty, 256);
         mbar_init(&bars->drain[0], 1);
         mbar_init(&bars->drain[1], 1);
+        mbar_init(&bars->stall, 1);
         bars->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -552,7 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         TileRec o{};
         uint64_t row_lse = 0, row_d = 0;  // query-major: this row's -lse * log2(e) and -D, twice
-        for (;; ++g) {
+        if (p.test_stall_us > 0)  // the wait runs out: status 3, and every role winds down
+            mbar_wait(&bars->stall, 0, abort_flag, dev_status, 1000ull * static_cast<uint64_t>(p.test_stall_us));
+        else for (;; ++g) {
             {
                 if (!wait(&bars->y0_full[y0.i], y0.lap)) break;  // (its record; the tile is long there)
                 const StepRec rec = bars->step[y0.i];
@@ -922,8 +926,9 @@ __global__ void __launch_bounds__(8 * kFewKeys) attn_bwd_sinks_starts_kernel(con
 // Block (document, kv head, 256 of the values): the sinks' rows of dk, dv of documents with far query
 // tiles, summed over the window's part and the pieces in order.
 __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const AttnProblem p, __nv_bfloat16* dk,
-                                                                __nv_bfloat16* dv, const WorkspaceHeader* hdr) {
-    if (hdr->status != DEV_OK) return;
+                                                                __nv_bfloat16* dv, const WorkspaceHeader* hdr,
+                                                                const int* call_status) {
+    if (hdr->status != DEV_OK || *call_status != DEV_OK) return;  // no list, or parts may be missing
     const int d = blockIdx.x, g = blockIdx.y, hd = p.head_dim;
     const int64_t a = static_cast<int64_t>(p.cu_seqlens[d]) * p.slot_mult;
     const int64_t slots = static_cast<int64_t>(p.cu_seqlens[d + 1]) * p.slot_mult - a;
@@ -1023,7 +1028,7 @@ cudaError_t launch_attn_bwd_sinks_dkdv(const AttnProblem& p, const CUtensorMap& 
                               stream);
     if (e != cudaSuccess || p.sinks == 0) return e;
     attn_bwd_sink_sum_kernel<<<dim3(p.batch, p.kv_heads, (p.sinks * 2 * p.head_dim + 255) / 256), 256, 0, stream>>>(
-        p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr);
+        p, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr, status);
     return cudaGetLastError();
 }
 

@@ -189,6 +189,7 @@ constexpr uint32_t kBoards = 4;
 
 struct GBars {
     TcBars t;
+    uint64_t stall;  // never signalled: the failure-detection test hook waits on it
     uint64_t item_full[kBoards], item_empty[kBoards];
     GBoard board[kBoards];
 };
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_init(&gbars->item_empty[i], 9);  // the MMA warp and 8 softmax warps
             }
             mbar_init(&bars->drain, 1);
+            mbar_init(&gbars->stall, 1);
             bars->abort = 0;
             fence_mbar_init();
             tma_prefetch_desc(&tm_q);
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const __nv_bfloat16* k_all = static_cast<const __nv_bfloat16*>(p.k) + unit * 8;
         const __nv_bfloat16* v_all = static_cast<const __nv_bfloat16*>(p.v) + unit * 8;
         const bool q_boxes = kBlockM % p.pack == 0;
-        uint32_t qc = 0, kc = 0;  // Q sub-tiles and key tiles issued
+        uint32_t qc = 0, kc = 0, vc = 0;  // Q sub-tiles, K tiles and V tiles issued
         bool ok = true;
         auto acquire = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
@@ -425,9 +427,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int head = it.chunk * p.pack / G;
             if (w == 0) ok = publish(&it);
             if (ok && it.active(0)) ok = load_q(it, 0);
-            for (int t = it.tb; ok && t < it.te; ++t, ++kc) {
+            for (int t = it.tb; ok && t < it.te; ++t) {
                 const int col0 = t * kBlockN;
-                const uint32_t sk = kc % L::kKStages, sv = kc % L::kVStages;
+                const uint32_t sk = kc % L::kKStages, sv = vc % L::kVStages;
                 // all 128 columns are window columns, or tokens of the sequence behind the last one
                 const int past = col0 + kBlockN - it.cols.n_w;
                 if (p.box_rows >= 8 && (past <= 0 || (it.cols.total == it.cols.n_w && past <= it.behind))) {
@@ -435,12 +437,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!ok) break;
                     if (w == 0) load_boxes(&tm_k, L::kOffK + sk * L::kKV, it, col0, head, &bars->k_full[sk], false);
                     else mbar_arrive(&bars->k_full[sk]);
-                    ok = acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
+                    ++kc;
+                    ok = acquire(&bars->v_empty[sv], ((vc / L::kVStages) & 1) ^ 1);
                     if (!ok) break;
                     const bool first = PAGED && t == 0 && it.ns < it.unseen;
                     if (w == 1) load_boxes(&tm_v, L::kOffV + sv * L::kKV, it, col0, head, &bars->v_full[sv], first);
                     else if (w == 2 && first) load_first(L::kOffV + sv * L::kKV, it, head, &bars->v_full[sv]);
                     else mbar_arrive(&bars->v_full[sv]);
+                    ++vc;
                 } else {
                     // documents: whole groups of 8 window columns by TMA, the rest row by row. (Pages: the lookups in
                     // between made it slower, 68 us instead of 63 for 24 sequences of 1 to 300 new tokens, 12 heads
@@ -465,12 +469,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         load_groups(&tm_k8, L::kOffK + sk * L::kKV, it.where + it.cols.lo + col0, groups, head, &bars->k_full[sk]);
                     load_rows(sbase + L::kOffK + sk * L::kKV, k_all, 8 * groups, idx[0], idx[1], idx[2], idx[3], head);
                     cp_async_arrive(&bars->k_full[sk]);
-                    ok = acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
+                    ++kc;
+                    ok = acquire(&bars->v_empty[sv], ((vc / L::kVStages) & 1) ^ 1);
                     if (!ok) break;
                     if (!PAGED && w == 1)
                         load_groups(&tm_v8, L::kOffV + sv * L::kKV, it.where + it.cols.lo + col0, groups, head, &bars->v_full[sv]);
                     load_rows(sbase + L::kOffV + sv * L::kKV, v_all, 8 * groups, idx[0], idx[1], idx[2], idx[3], head);
                     cp_async_arrive(&bars->v_full[sv]);
+                    ++vc;
                 }
                 // the second sub-tile's Q after the first key tile: its slot is free only when the previous
                 // item's epilogue is through, and the first sub-tile can start without it
@@ -480,11 +486,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (ok && w == 0) ok = publish(nullptr);
         cp_async_wait_all();
         if (!ok && lane == 0) {
-            // Wait (bounded) for the TMA copies issued last into every buffer.
-            for (uint32_t n = kc > L::kKStages ? kc - L::kKStages : 0; n < kc; ++n) {
-                drain_wait(&bars->k_full[n % L::kKStages], (n / L::kKStages) & 1);
-                drain_wait(&bars->v_full[n % L::kVStages], (n / L::kVStages) & 1);
-            }
+            // Wait for the TMA copies issued last into every buffer, with one limit for all: a barrier whose other
+            // loaders gave up before they arrived never completes.
+            const uint64_t t0 = globaltimer_ns();
+            auto drain = [&](uint64_t* bars_of, uint32_t ring, uint32_t issued) {
+                for (uint32_t n = issued > ring ? issued - ring : 0; n < issued; ++n)
+                    while (!mbar_test(&bars_of[n % ring], (n / ring) & 1) && globaltimer_ns() - t0 <= kWaitLimitNs) {}
+            };
+            drain(bars->q_full, L::kQSlots, qc);
+            drain(bars->k_full, L::kKStages, kc);
+            drain(bars->v_full, L::kVStages, vc);
         }
         __syncwarp();
     } else if (warp == 8) {
@@ -633,6 +644,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t pv_seen = 0;  // hd 64: P V completions of this sub-tile awaited so far
         uint32_t q_seq = 0;    // index of the current item's first Q sub-tile in this CTA's stream
         bool ok = true;
+        if (p.test_stall_us > 0)  // the wait runs out: status 3, and every role winds down
+            ok = __all_sync(0xffffffffu, mbar_wait(&gbars->stall, 0, abort_flag, dev_status,
+                                                   1000ull * static_cast<uint64_t>(p.test_stall_us)));
         // the low n bits (n clamped to 0 .. 32)
         auto low_bits = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); };
         for (uint32_t ic = 0; ok; ++ic) {
@@ -846,6 +860,7 @@ __device__ __forceinline__ bool at_or_before(int4 a, int x, int chunk, int t) {
 template <int HD>
 __global__ void __launch_bounds__(256) attn_join_cuts_kernel(GatherProblem p, int p_inv) {
     grid_dep_wait();
+    if (p.hdr->status == DEV_TIMEOUT) return;  // parts may be missing
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int4 cut = p.starts[c + 1];
     if (cut.z == 0 || !at_or_before(p.starts[c], cut.x, cut.y, 0)) return;

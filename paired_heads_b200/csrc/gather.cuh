@@ -51,6 +51,7 @@ struct GatherProblem {
     int pack, tile_tokens;
     int box_rows;            // rows of a TMA box over k / v; paged: they lie in one page, and columns
                              // begin at multiples of it (1: no TMA)
+    int test_stall_us;       // test hook: > 0 makes the softmax warps wait that long for nothing
 };
 
 // One row tile: up to 256 rows (two sub-tiles) of one sequence, times each chunk of `pack` heads.

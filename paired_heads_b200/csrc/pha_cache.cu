@@ -309,13 +309,18 @@ size_t pha_attn_paged_workspace_bytes(int batch, int max_q, int max_kv, int tota
                : 0;
 }
 
-pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages,
-                              const int32_t* page_table, int max_pages, int n_pages, int page_size,
-                              const int32_t* cu_seqlens, const int32_t* kv_lens, int batch,
-                              int max_q, int max_kv, int total_q, int n_heads, int n_kv_heads,
-                              int head_dim, pha_dtype dtype, int window, int sinks, int paired,
-                              float scale, void* o, float* lse, void* workspace,
-                              size_t workspace_bytes, int32_t* status, pha_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// stall_us: test hook, see pha_test_attn_paged_fwd_stalled.
+pha_status paged_fwd(const void* q, const void* k_pages, const void* v_pages,
+                     const int32_t* page_table, int max_pages, int n_pages, int page_size,
+                     const int32_t* cu_seqlens, const int32_t* kv_lens, int batch,
+                     int max_q, int max_kv, int total_q, int n_heads, int n_kv_heads,
+                     int head_dim, pha_dtype dtype, int window, int sinks, int paired,
+                     float scale, void* o, float* lse, void* workspace,
+                     size_t workspace_bytes, int32_t* status, pha_stream_t stream, int stall_us) {
     const int shift = log2_exact(page_size);
     if ((dtype != PHA_BF16 && dtype != PHA_F32) || shift < 0 || shift > 24 || n_pages <= 0 ||
         max_pages <= 0 || !(scale == scale) || !aligned(status, 4) || !aligned(lse, 4))
@@ -333,7 +338,9 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
         !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
         return PHA_ERR_INVALID;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes) return PHA_ERR_WORKSPACE;
+    if (stall_us != 0 && !w.gather) return PHA_ERR_UNSUPPORTED;  // (the other kernels have no waits)
     GatherProblem p{};
+    p.test_stall_us = stall_us;
     p.q = q;
     p.k = k_pages;
     p.v = v_pages;
@@ -387,6 +394,37 @@ pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_
         return PHA_ERR_CUDA;
     if (w.tiles == 0) return PHA_OK;  // no new tokens are allowed for: the plan has checked the lengths
     return of(launch_attn_gather(p, tq, tk, tv, tk, tv, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+pha_status pha_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* page_table, int max_pages, int n_pages, int page_size,
+                              const int32_t* cu_seqlens, const int32_t* kv_lens, int batch,
+                              int max_q, int max_kv, int total_q, int n_heads, int n_kv_heads,
+                              int head_dim, pha_dtype dtype, int window, int sinks, int paired,
+                              float scale, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, int32_t* status, pha_stream_t stream) {
+    return paged_fwd(q, k_pages, v_pages, page_table, max_pages, n_pages, page_size, cu_seqlens, kv_lens, batch,
+                     max_q, max_kv, total_q, n_heads, n_kv_heads, head_dim, dtype, window, sinks, paired, scale, o,
+                     lse, workspace, workspace_bytes, status, stream, 0);
+}
+
+pha_status pha_test_attn_paged_fwd_stalled(const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, int max_pages, int n_pages,
+                                           int page_size, const int32_t* cu_seqlens,
+                                           const int32_t* kv_lens, int batch, int max_q, int max_kv,
+                                           int total_q, int n_heads, int n_kv_heads, int head_dim,
+                                           pha_dtype dtype, int window, int sinks, int paired,
+                                           float scale, void* o, float* lse, void* workspace,
+                                           size_t workspace_bytes, int32_t* status, int stall_us,
+                                           pha_stream_t stream) {
+    if (stall_us < 1 || stall_us > 100000) return PHA_ERR_INVALID;
+    return paged_fwd(q, k_pages, v_pages, page_table, max_pages, n_pages, page_size, cu_seqlens, kv_lens, batch,
+                     max_q, max_kv, total_q, n_heads, n_kv_heads, head_dim, dtype, window, sinks, paired, scale, o,
+                     lse, workspace, workspace_bytes, status, stream, stall_us);
 }
 
 }  // extern "C"

@@ -123,11 +123,16 @@ size_t pha_attn_sinks_bwd_workspace_bytes(int batch, int max_len, int total_toke
     return bwd_plan(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, window, sinks, paired).bytes;
 }
 
-pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
-                              const int32_t* cu_seqlens, int batch, int max_len, int total_tokens,
-                              int n_heads, int n_kv_heads, int head_dim, pha_dtype dtype,
-                              int window, int sinks, int paired, float scale, void* o, float* lse,
-                              void* workspace, size_t workspace_bytes, pha_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// stall_us: test hook, see pha_test_attn_sinks_fwd_stalled.
+pha_status sinks_fwd(const void* q, const void* k, const void* v,
+                     const int32_t* cu_seqlens, int batch, int max_len, int total_tokens,
+                     int n_heads, int n_kv_heads, int head_dim, pha_dtype dtype,
+                     int window, int sinks, int paired, float scale, void* o, float* lse,
+                     void* workspace, size_t workspace_bytes, pha_stream_t stream, int stall_us) {
     const pha_status st = shape_status(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, dtype,
                                        sinks, paired, scale);
     if (st != PHA_OK) return st;
@@ -141,6 +146,7 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
                                                          window, sinks, paired))
         return PHA_ERR_WORKSPACE;
     GatherProblem p{};
+    p.test_stall_us = stall_us;
     p.q = q;
     p.k = k;
     p.v = v;
@@ -184,12 +190,12 @@ pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
     return of(launch_attn_gather(p, tq, tk, tv, tk8, tv8, stream));
 }
 
-pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const void* o,
-                              const float* lse, const void* dout, const int32_t* cu_seqlens,
-                              int batch, int max_len, int total_tokens, int n_heads,
-                              int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks,
-                              int paired, float scale, void* dq, void* dk, void* dv,
-                              void* workspace, size_t workspace_bytes, pha_stream_t stream) {
+pha_status sinks_bwd(const void* q, const void* k, const void* v, const void* o,
+                     const float* lse, const void* dout, const int32_t* cu_seqlens,
+                     int batch, int max_len, int total_tokens, int n_heads,
+                     int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks,
+                     int paired, float scale, void* dq, void* dk, void* dv,
+                     void* workspace, size_t workspace_bytes, pha_stream_t stream, int stall_us) {
     const pha_status st = shape_status(batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, dtype,
                                        sinks, paired, scale);
     if (st != PHA_OK) return st;
@@ -205,6 +211,7 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
                                                              n_kv_heads, head_dim, window, sinks, paired))
         return PHA_ERR_WORKSPACE;
     AttnProblem p{};
+    p.test_stall_us = stall_us;
     p.q = q;
     p.k = k;
     p.v = v;
@@ -260,6 +267,64 @@ pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const
         return PHA_ERR_CUDA;
     return of(launch_attn_bwd_sinks_dkdv(p, tq, tk, tv, tdo, tdk, tdv, nlse, dsum, dk, dv, list(w.keys), hdr_k,
                                          &hdr->status, stream));  // (one status word for the call)
+}
+
+pha_status stall_status(int stall_us, pha_dtype dtype) {
+    if (stall_us < 1 || stall_us > 100000) return PHA_ERR_INVALID;
+    return dtype == PHA_F32 ? PHA_ERR_UNSUPPORTED : PHA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pha_status pha_attn_sinks_fwd(const void* q, const void* k, const void* v,
+                              const int32_t* cu_seqlens, int batch, int max_len, int total_tokens,
+                              int n_heads, int n_kv_heads, int head_dim, pha_dtype dtype,
+                              int window, int sinks, int paired, float scale, void* o, float* lse,
+                              void* workspace, size_t workspace_bytes, pha_stream_t stream) {
+    return sinks_fwd(q, k, v, cu_seqlens, batch, max_len, total_tokens, n_heads, n_kv_heads, head_dim, dtype,
+                     window, sinks, paired, scale, o, lse, workspace, workspace_bytes, stream, 0);
+}
+
+pha_status pha_attn_sinks_bwd(const void* q, const void* k, const void* v, const void* o,
+                              const float* lse, const void* dout, const int32_t* cu_seqlens,
+                              int batch, int max_len, int total_tokens, int n_heads,
+                              int n_kv_heads, int head_dim, pha_dtype dtype, int window, int sinks,
+                              int paired, float scale, void* dq, void* dk, void* dv,
+                              void* workspace, size_t workspace_bytes, pha_stream_t stream) {
+    return sinks_bwd(q, k, v, o, lse, dout, cu_seqlens, batch, max_len, total_tokens, n_heads, n_kv_heads,
+                     head_dim, dtype, window, sinks, paired, scale, dq, dk, dv, workspace, workspace_bytes,
+                     stream, 0);
+}
+
+pha_status pha_test_attn_sinks_fwd_stalled(const void* q, const void* k, const void* v,
+                                           const int32_t* cu_seqlens, int batch, int max_len,
+                                           int total_tokens, int n_heads, int n_kv_heads,
+                                           int head_dim, pha_dtype dtype, int window, int sinks,
+                                           int paired, float scale, void* o, float* lse,
+                                           void* workspace, size_t workspace_bytes, int stall_us,
+                                           pha_stream_t stream) {
+    const pha_status st = stall_status(stall_us, dtype);
+    return st != PHA_OK ? st
+                        : sinks_fwd(q, k, v, cu_seqlens, batch, max_len, total_tokens, n_heads, n_kv_heads,
+                                    head_dim, dtype, window, sinks, paired, scale, o, lse, workspace,
+                                    workspace_bytes, stream, stall_us);
+}
+
+pha_status pha_test_attn_sinks_bwd_stalled(const void* q, const void* k, const void* v,
+                                           const void* o, const float* lse, const void* dout,
+                                           const int32_t* cu_seqlens, int batch, int max_len,
+                                           int total_tokens, int n_heads, int n_kv_heads,
+                                           int head_dim, pha_dtype dtype, int window, int sinks,
+                                           int paired, float scale, void* dq, void* dk, void* dv,
+                                           void* workspace, size_t workspace_bytes, int stall_us,
+                                           pha_stream_t stream) {
+    const pha_status st = stall_status(stall_us, dtype);
+    return st != PHA_OK ? st
+                        : sinks_bwd(q, k, v, o, lse, dout, cu_seqlens, batch, max_len, total_tokens, n_heads,
+                                    n_kv_heads, head_dim, dtype, window, sinks, paired, scale, dq, dk, dv,
+                                    workspace, workspace_bytes, stream, stall_us);
 }
 
 }  // extern "C"

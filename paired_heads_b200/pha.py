@@ -83,6 +83,10 @@ _lib.pha_attn_paged_workspace_bytes.argtypes = [_i] * 11
 _lib.pha_attn_paged_workspace_bytes.restype = _sz
 _lib.pha_attn_paged_fwd.argtypes = [_p] * 4 + [_i] * 3 + [_p, _p] + [_i] * 11 + [_f32, _p, _p, _p,
                                                                                _sz, _p, _p]
+_lib.pha_test_attn_sinks_fwd_stalled.argtypes = [_p] * 4 + [_i] * 10 + [_f32, _p, _p, _p, _sz, _i, _p]
+_lib.pha_test_attn_sinks_bwd_stalled.argtypes = [_p] * 7 + [_i] * 10 + [_f32, _p, _p, _p, _p, _sz, _i, _p]
+_lib.pha_test_attn_paged_fwd_stalled.argtypes = [_p] * 4 + [_i] * 3 + [_p, _p] + [_i] * 11 + [
+    _f32, _p, _p, _p, _sz, _p, _i, _p]
 _lib.pha_cache_append.argtypes = [_p] * 5 + [_i] * 3 + [_p, _p] + [_i] * 5 + [_p, _p]
 _lib.pha_cache_workspace_bytes.argtypes = [_i, _i]
 _lib.pha_cache_workspace_bytes.restype = _sz
@@ -94,7 +98,8 @@ _lib.pha_cache_trim.argtypes = [_p, _i, _p, _i, _p] + [_i] * 5 + [_p, _p]
 _lib.pha_cache_compact.argtypes = [_p, _i, _i, _p, _i, _p, _p, _i, _sz, _p, _sz, _p, _p]
 for _f in ("pha_attn_sinks_fwd", "pha_attn_sinks_bwd", "pha_attn_paged_fwd", "pha_cache_append",
            "pha_cache_fork", "pha_cache_reserve", "pha_cache_free", "pha_cache_trim",
-           "pha_cache_compact"):
+           "pha_cache_compact", "pha_test_attn_sinks_fwd_stalled", "pha_test_attn_sinks_bwd_stalled",
+          "pha_test_attn_paged_fwd_stalled"):
     getattr(_lib, _f).restype = _i
 for _f in ("pha_rope_tables", "pha_rope", "pha_attn_fwd", "pha_attn_status",
            "pha_attn_fwd_noalloc", "pha_test_attn_fwd_stalled", "pha_attn_fwd_fp8", "pha_qk_norm_rope", "pha_attn_fwd_aux_v", "pha_rope_bwd",
@@ -574,6 +579,47 @@ def pha_attn_paged_fwd(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, max
           n_pages, page, cu_seqlens.data_ptr(), kv_lens.data_ptr(), batch, max_q, max_kv, t, h,
           hkv, hd, code, window, sinks, paired, scale, o.data_ptr(), _ptr(lse),
           workspace.data_ptr(), _nbytes(workspace), _ptr(status)), stream)
+
+
+def pha_test_attn_sinks_fwd_stalled(q, k, v, cu_seqlens, max_len: int, o, lse, workspace, stall_us: int,
+                                    *, window: int, sinks: int, paired: bool = False, scale: float = 0.0,
+                                    stream=None):
+    """Failure-detection test hook: pha_attn_sinks_fwd whose softmax warps first wait stall_us
+    microseconds on a barrier that nothing signals (device status 3, no row written)."""
+    t, h, hkv, hd, _, code = _dims(q, k)
+    _check("pha_test_attn_sinks_fwd_stalled",
+           _lib.pha_test_attn_sinks_fwd_stalled(
+               _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), cu_seqlens.shape[0] - 1, max_len, t, h, hkv, hd,
+               code, window, sinks, int(paired), float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+               _nbytes(workspace), int(stall_us), _stream(stream, q)))
+
+
+def pha_test_attn_sinks_bwd_stalled(q, k, v, o, lse, dout, cu_seqlens, max_len: int, dq, dk, dv,
+                                    workspace, stall_us: int, *, window: int, sinks: int,
+                                    paired: bool = False, scale: float = 0.0, stream=None):
+    """The same of pha_attn_sinks_bwd."""
+    t, h, hkv, hd, _, code = _dims(q, k)
+    _check("pha_test_attn_sinks_bwd_stalled",
+           _lib.pha_test_attn_sinks_bwd_stalled(
+               _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(cu_seqlens),
+               cu_seqlens.shape[0] - 1, max_len, t, h, hkv, hd, code, window, sinks, int(paired), float(scale),
+               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _nbytes(workspace), int(stall_us),
+               _stream(stream, q)))
+
+
+def pha_test_attn_paged_fwd_stalled(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, max_q: int,
+                                    max_kv: int, o, lse, workspace, stall_us: int, *, window: int = 0,
+                                    sinks: int = 0, paired: bool = False, scale: float = 0.0,
+                                    status=None, stream=None):
+    """The same of pha_attn_paged_fwd (more than 16 rows a sequence)."""
+    t, h, hkv, hd, _, code = _dims(q, k_pages)
+    batch, max_pages = page_table.shape
+    _check("pha_test_attn_paged_fwd_stalled",
+           _lib.pha_test_attn_paged_fwd_stalled(
+               _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), max_pages, k_pages.shape[0],
+               k_pages.shape[1], _ptr(cu_seqlens), _ptr(kv_lens), batch, max_q, max_kv, t, h, hkv, hd, code,
+               window, sinks, int(paired), float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+               _nbytes(workspace), _ptr(status), int(stall_us), _stream(stream, q)))
 
 
 def pha_cache_append(k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, *, status=None,

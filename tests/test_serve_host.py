@@ -297,3 +297,29 @@ def test_windows_past_32_bits_do_not_wrap(pha, monkeypatch):
                          pha.pha_attn_paged_workspace_bytes(1, 1, 90000, 1, 2, 2, 64, torch.bfloat16, window=w, sinks=s))
     assert size(2 ** 32 + 5, 1) == size(0, 1) != size(5, 1)
     assert size(5, 2 ** 32 + 4)[:2] == (0, 0) and size(5, 2 ** 32 + 4)[2] == size(0, 0)[2]
+
+
+def test_stall_hooks_argument_errors(pha):
+    """Failure-detection hooks: the limits of the stall, then the checks of the call itself."""
+    lib, f = pha.library(), ctypes.c_float(0.0)
+    for n in ("pha_test_attn_sinks_fwd_stalled", "pha_test_attn_sinks_bwd_stalled", "pha_test_attn_paged_fwd_stalled"):
+        assert n in pha.exported_symbols()
+
+    def fwd(us, dtype=0, sinks=4, ws=A):
+        return lib.pha_test_attn_sinks_fwd_stalled(A, A, A, A, 1, 128, 128, 4, 4, 64, dtype, 64, sinks, 0, f, A, A, ws,
+                                                   10, us, None)
+
+    def bwd(us, dtype=0, sinks=4, ws=A):
+        return lib.pha_test_attn_sinks_bwd_stalled(A, A, A, A, A, A, A, 1, 128, 128, 4, 4, 64, dtype, 64, sinks, 0, f,
+                                                   A, A, A, ws, 10, us, None)
+
+    def paged(us, dtype=0, max_q=100, sinks=4, ws=A, size=10):
+        return lib.pha_test_attn_paged_fwd_stalled(A, A, A, A, 8, 64, 16, A, A, 2, max_q, 128, 128, 4, 4, 64, dtype, 64,
+                                                   sinks, 0, f, A, A, ws, size, None, us, None)
+
+    for call in (fwd, bwd, paged):
+        assert call(0) == call(-1) == call(100001) == -1
+        assert call(1) == call(100000) == -3               # everything fits but the workspace
+        assert call(5, sinks=-1) == -1 and call(5, ws=None) == -3
+    assert fwd(5, dtype=1) == bwd(5, dtype=1) == -2        # float32 has no waits
+    assert paged(5, dtype=1, size=1 << 40) == -2 and paged(5, max_q=4, size=1 << 40) == -2
