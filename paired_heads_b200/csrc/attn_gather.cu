@@ -65,9 +65,8 @@ struct GItem {
     bool begins;         // its first key tile is among them
     GatherCols cols;
     int ns;              // columns below it are sinks that lie in the window part
-    int unseen;          // pages: columns [ns, unseen) of the first box lie below every window and are no
-                         // sinks: there to begin at a box. Their scores are masked; their values, which may be
-                         // anything (NaN times a zero weight is NaN), are left out
+    int unseen;          // pages: columns [ns, unseen) lie below every window and are no sinks: there to begin at
+                         // a box
     int sf, sl;          // tiles [sf, sl] hold the sink columns
     int nr[2];           // rows of sub-tile r
     int wf[2], wl[2];    // window tiles of sub-tile r
@@ -182,6 +181,7 @@ __device__ __forceinline__ GItem decode_gather(const GWalk& wk, const GatherProb
 struct GBoard {
     int last_one;  // the share is over; nothing else is valid
     int q0, chunk, pos0, tb, te, whole, begins, lo, n_w, total, ns, sf, sl;
+    int unseen;
     int nr[2], wf[2], wl[2], first[2], last[2];
     int t_full[2], t_end[2];  // tiles [t_full, t_end) of sub-tile r need no mask
 };
@@ -318,12 +318,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         // 128 consecutive columns by TMA, a lane per box; a page that is none reads as zeros (a row behind
         // the pool). Every loader thread arrives once per tile: here one of them with the bytes to come.
-        // skip: the first box is left to load_first.
-        auto load_boxes = [&](const CUtensorMap* map, int off, const GItem& it, int col0, int head, uint64_t* bar,
-                              bool skip) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, L::kKV - (skip ? p.box_rows * HD * 2 : 0));
+        auto load_boxes = [&](const CUtensorMap* map, int off, const GItem& it, int col0, int head, uint64_t* bar) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, L::kKV);
             else mbar_arrive(bar);
-            if (lane * p.box_rows < kBlockN && !(skip && lane == 0)) {
+            if (lane * p.box_rows < kBlockN) {
                 int64_t row = key_row<PAGED>(p, it.where, it.where, it.cols.lo + col0 + lane * p.box_rows);
                 if (PAGED && row < 0) {
                     row = static_cast<int64_t>(p.n_pages) << p.page_shift;
@@ -335,20 +333,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 static_cast<int>(row), bar);
             }
             __syncwarp();
-        };
-        // Pages: the values of an item's first box row by row, zeros for columns [ns, unseen) (see GItem), by the
-        // warp that plain tiles leave idle (79.1 us instead of 77.5 for 24 sequences of 1 to 300 new tokens, 12
-        // heads of 64, window 1024, 16 sinks, where that box came by TMA as it was).
-        auto load_first = [&](int off, const GItem& it, int head, uint64_t* bar) {
-            const int64_t row0 = key_row<PAGED>(p, it.where, it.where, it.cols.lo);
-            if (row0 < 0 && p.status && lane == 0) atomicMax(p.status, DEV_BAD_PAGE);
-#pragma unroll 2
-            for (int j = row_in; j < p.box_rows; j += kRpi) {
-                const bool seen = row0 >= 0 && (j < it.ns || j >= it.unseen);
-                const int64_t at = ((seen ? row0 + j : 0) * p.kv_heads + head) * HD;
-                cp_async_16_zfill(place(smem_u32(smem + off), j), v_all + at, seen ? 16u : 0u);
-            }
-            cp_async_arrive(bar);
         };
         // query sub-tile r of an item
         auto load_q = [&](const GItem& it, int r) -> bool {
@@ -402,6 +386,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     b.n_w = it->cols.n_w;
                     b.total = it->cols.total;
                     b.ns = it->ns;
+                    b.unseen = it->unseen;
                     b.sf = it->sf;
                     b.sl = it->sl;
 #pragma unroll
@@ -435,14 +420,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (p.box_rows >= 8 && (past <= 0 || (it.cols.total == it.cols.n_w && past <= it.behind))) {
                     ok = acquire(&bars->k_empty[sk], ((kc / L::kKStages) & 1) ^ 1);
                     if (!ok) break;
-                    if (w == 0) load_boxes(&tm_k, L::kOffK + sk * L::kKV, it, col0, head, &bars->k_full[sk], false);
+                    if (w == 0) load_boxes(&tm_k, L::kOffK + sk * L::kKV, it, col0, head, &bars->k_full[sk]);
                     else mbar_arrive(&bars->k_full[sk]);
                     ++kc;
                     ok = acquire(&bars->v_empty[sv], ((vc / L::kVStages) & 1) ^ 1);
                     if (!ok) break;
-                    const bool first = PAGED && t == 0 && it.ns < it.unseen;
-                    if (w == 1) load_boxes(&tm_v, L::kOffV + sv * L::kKV, it, col0, head, &bars->v_full[sv], first);
-                    else if (w == 2 && first) load_first(L::kOffV + sv * L::kKV, it, head, &bars->v_full[sv]);
+                    if (w == 1) load_boxes(&tm_v, L::kOffV + sv * L::kKV, it, col0, head, &bars->v_full[sv]);
                     else mbar_arrive(&bars->v_full[sv]);
                     ++vc;
                 } else {
@@ -457,7 +440,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int kk = 0; kk < 4; ++kk) {
                         const int col = col0 + 32 * kk + lane;
                         idx[kk] = -1;
-                        if (col >= col0 + 8 * groups && col < it.cols.total && (!PAGED || col < it.ns || col >= it.unseen)) {
+                        if (col >= col0 + 8 * groups && col < it.cols.total) {
                             const int64_t row = key_row<PAGED>(p, it.where, it.where, col_pos(it.cols, col));
                             if (row < 0 && p.status) atomicMax(p.status, DEV_BAD_PAGE);
                             idx[kk] = static_cast<int>(row);
@@ -508,6 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool pend[2] = {false, false}, pend_first[2] = {false, false}, pend_last[2] = {false, false};
         uint32_t qc = 0;  // Q sub-tiles of the segments before the current one
         uint32_t g = 0;   // index of the current key tile in this CTA's stream
+        int z_lo = 0, z_hi = 0;  // pages: rows of V_{g-1} that no query sees
         bool ok = true, more = true;
         for (uint32_t ic = 0; ok && more; ++ic) {
             const uint32_t ib = ic % kBoards;
@@ -518,6 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             more = !uniform(bd.last_one);  // behind the last segment: one more turn, for the last P V
             const int tb = more ? uniform(bd.tb) : 0, te = more ? uniform(bd.te) : (g > 0 ? 1 : 0);
             const int sf = uniform(bd.sf), sl = uniform(bd.sl);
+            const int ns = PAGED ? uniform(bd.ns) : 0, unseen = PAGED ? uniform(bd.unseen) : 0;
             int nr[2], wf[2], wl[2], first[2], last[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -541,7 +526,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t n = g - 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[n % L::kVStages], (n / L::kVStages) & 1, abort_flag, dev_status));
                     if (!ok) break;
-                    fence_proxy_async_smem();  // gathered rows were written by cp.async; the MMA reads them next
+                    if (PAGED && z_lo < z_hi) {
+                        // Their scores are masked, but their values may be anything, and NaN times a zero weight is
+                        // NaN: zeros instead (a row is 128 bytes of each chunk). (Fetching that box row by row, with
+                        // zeros for them: 80.2 us, this 78.9, neither 77.9, 24 sequences of 1 to 300 new tokens, 12
+                        // heads of 64, window 1024, 16 sinks.)
+                        uint8_t* v = smem + L::kOffV + (n % L::kVStages) * L::kKV + z_lo * 128;
+#pragma unroll 1
+                        for (int x = lane; x < (z_hi - z_lo) * 8; x += 32)
+#pragma unroll
+                            for (int c = 0; c < HD / 64; ++c)
+                                *reinterpret_cast<uint4*>(v + c * L::kChunk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        z_hi = 0;
+                    }
+                    fence_proxy_async_smem();  // rows written by cp.async and above; the MMA reads them next
                 }
                 const uint32_t sk = g % L::kKStages;
                 if (more) {
@@ -621,6 +619,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     umma_commit(&bars->k_empty[sk]);
                 }
                 __syncwarp();
+                if (PAGED && t == 0) {
+                    z_lo = ns > 0 ? ns : 0;
+                    z_hi = unseen;
+                }
                 ++g;
             }
         }
