@@ -24,8 +24,10 @@
 // products, as in attn_bwd_tc.cu: 798 us for dK / dV of 2 x 8192 tokens, 32 / 8 heads of 128, window
 // 1024, 675 for dQ; the two column halves of a step staggered instead: 680 and 574, the halves' N = 64
 // products reading X twice; this one: 530 and 367, 3,700 and 2,500 clocks a step.) What is left over the
-// products' 2,050 and 1,540 clocks is the chain S -> P -> dV -> next S, P lying in S's columns: with 256
-// columns of accumulators TMEM has no room for a second S.
+// products' 2,050 and 1,540 clocks is the chain S -> P -> dV -> next S, P lying in S's columns. At hd 128 the
+// key-major kernel has no room for a second S: S, dP, dV and dK take all 512 columns of TMEM. The query-major one spends
+// its last 128 on two buffers of dS instead, and hd 64 (accumulators of 128 columns or 64) is laid out alike: there a
+// second S would fit and has not been tried.
 // TMEM columns: S [0, 128), dP [128, 256), accumulators from 256 (dV, dK or dQ). Key-major, P^T and dS^T
 // of column half h (bf16 A operands) overwrite the first 32 of the half's own S or dP columns;
 // query-major, dS goes to two buffers of 64 columns at 384 so that S and dP of the next step wait only

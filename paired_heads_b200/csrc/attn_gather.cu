@@ -2,8 +2,8 @@
 // sliding window and sinks, keys in packed documents or in the pages of a cache.
 //
 // Mathematics: o = softmax(scale q k^T) v row by row over the visible key columns (gather.cuh), one
-// pass with a running maximum and sum; a split of the columns leaves normalised partial rows and their
-// log-sum-exp for attn_join_kernel.
+// pass with a running maximum and sum; an item that a cut between two CTAs' shares divides leaves
+// normalised partial rows and their log-sum-exp, two places a CTA, for attn_join_cuts_kernel.
 //
 // A row tile is up to 256 rows, two sub-tiles of 128: `pack` query heads of one kv head's group times
 // tile_tokens tokens. Packing the group multiplies the rows that each loaded key tile serves and lets

@@ -147,12 +147,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_join_kernel(GatherProblem
     if (b < 0) return;
     const GatherSeq s = gather_seq(p, b);
     if (!s.ok || slot >= s.q0 + s.n_q) return;
-    int n = p.n_splits;
-    if (p.split_keys > 0) {
-        const GatherCols all = gather_cols(p, s.kv - s.n_q, s.n_q);
-        n = (all.total + p.split_keys - 1) / p.split_keys;
-        if (n <= 1) return;  // written by its only split
-    }
+    const GatherCols all = gather_cols(p, s.kv - s.n_q, s.n_q);
+    const int n = (all.total + p.split_keys - 1) / p.split_keys;
+    if (n <= 1) return;  // written by its only split
     float top = -INFINITY;
     for (int i = 0; i < n; ++i) top = fmaxf(top, p.part_lse[i * rows + row]);
     float acc[kMaxDim / 32] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
