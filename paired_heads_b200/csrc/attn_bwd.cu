@@ -145,13 +145,16 @@ __device__ __forceinline__ void store_row(T* dst, const float4 (&x)[NC], int hd,
     }
 }
 
-template <int HP, typename T>
+// SINKS: the backward of attention with sinks (p.checked is set). Apart, because the loop has no registers to
+// spare at hd 128: with its tests in every call pha_attn_bwd took 1,726 us instead of 1,543 (8 documents of 512
+// tokens, 8 / 2 heads of 128, float32; 1,017 instead of 930 for 8 paired ones of 1,024, 6 heads, window 128).
+template <int HP, typename T, bool SINKS>
 __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
                                                                    const T* __restrict__ dout,
                                                                    const float* __restrict__ dsum,
                                                                    T* __restrict__ dq) {
     constexpr int NC = HP / (4 * kLanesPerRow);
-    if (p.checked && p.checked->status != DEV_OK) return;
+    if (SINKS && p.checked->status != DEV_OK) return;
     extern __shared__ float4 bsm4[];
     float* ks = reinterpret_cast<float*>(bsm4);  // [kStage][HP]
     float* vs = ks + kStage * HP;                // [kStage][HP]
@@ -173,18 +176,19 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
             j1 = i + 1;
             if (p.window > 0 && i - p.window + 1 > j0) j0 = i - p.window + 1;
             // with sinks: dS = P (dP - D) of a query that sees one key alone is 0, not the two sums' rounding
-            if (p.checked && j1 - j0 == 1 && (p.sinks == 0 || j0 == lo)) j1 = j0;
+            if (SINKS && j1 - j0 == 1 && (p.sinks == 0 || j0 == lo)) j1 = j0;
         }
     }
     if (threadIdx.x == 0) {
-        range[0] = range[2] = LLONG_MAX;
+        range[0] = LLONG_MAX;
+        if (SINKS) range[2] = LLONG_MAX;
         range[1] = LLONG_MIN;
     }
     __syncthreads();
     if (in_doc && r8 == 0) {
         atomicMin(&range[0], j0);
         atomicMax(&range[1], j1);
-        atomicMin(&range[2], static_cast<long long>(lo));
+        if (SINKS) atomicMin(&range[2], static_cast<long long>(lo));
     }
     const int64_t row = i * H + h;
     float4 qi[NC], gi[NC], acc[NC];
@@ -199,27 +203,28 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
     const long long J0 = range[0], J1 = range[1];
     // Sinks below every row's window: those of the block's first document (any later document
     // starts inside the block, so its sinks are window keys of some row or lie in [J0, J1)).
-    const long long E0 = p.sinks > 0 ? range[2] : J0;
-    const long long E1 = min(E0 + p.sinks, J0);
+    const int sinks = SINKS ? p.sinks : 0;
+    const long long E0 = sinks > 0 ? range[2] : J0;
+    const long long E1 = min(E0 + sinks, J0);
     const T* kg = static_cast<const T*>(p.k) + static_cast<int64_t>(g) * hd;
     const T* vg = static_cast<const T*>(p.v) + static_cast<int64_t>(g) * hd;
     const int64_t kstride = static_cast<int64_t>(Hkv) * hd;
     const float d = in_doc ? dsum[row] : 0.f;
     {
         int n;
-        for (long long c0 = E0 < E1 ? E0 : J0; c0 < J1; c0 = (c0 < E1 && c0 + n >= E1) ? J0 : c0 + n) {
-            const long long end = c0 < E1 ? E1 : J1;
+        for (long long c0 = SINKS && E0 < E1 ? E0 : J0; c0 < J1;
+             c0 = !SINKS ? c0 + kStage : (c0 < E1 && c0 + n >= E1 ? J0 : c0 + n)) {
+            const long long end = SINKS && c0 < E1 ? E1 : J1;
             n = static_cast<int>(end - c0 < kStage ? end - c0 : kStage);
             __syncthreads();  // every warp is done with the previous chunk
             stage_rows<HP>(ks, kg, c0, n, kstride, hd);
             stage_rows<HP>(vs, vg, c0, n, kstride, hd);
             __syncthreads();
-            if ((c0 + n <= wj0 && p.sinks == 0) || c0 >= wj1) continue;  // warp-uniform
+            if ((c0 + n <= wj0 && sinks == 0) || c0 >= wj1) continue;  // warp-uniform
             // only what the warp's rows see of the chunk
-            const int from = p.sinks == 0 && wj0 > c0 ? static_cast<int>(wj0 - c0) : 0;
+            const int from = sinks == 0 && wj0 > c0 ? static_cast<int>(wj0 - c0) : 0;
             const int to = wj1 < c0 + n ? static_cast<int>(wj1 - c0) : n;
-#pragma unroll kUnroll<HP>
-            for (int jj = from; jj < to; ++jj) {
+            const auto pair = [&](int jj) {
                 const long long j = c0 + jj;
                 const float4* kr = reinterpret_cast<const float4*>(ks + jj * HP);
                 const float4* vr = reinterpret_cast<const float4*>(vs + jj * HP);
@@ -232,25 +237,27 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dq_kernel(AttnProblem p,
                     dp = dot4(gi[t], vr[r8 + kLanesPerRow * t], dp);
                 }
                 group_sum2(s, dp);
-                const bool vis = j < j1 && (j >= j0 || (j >= lo && j < lo + p.sinks));
+                const bool vis = (j >= j0 && j < j1) || (SINKS && j >= lo && j < lo + sinks && j < j1);
                 const float pij = vis ? exp2f(fmaf(s, scale2, -lse2)) : 0.f;
                 const float ds = pij * (dp - d) * p.scale;
 #pragma unroll
                 for (int t = 0; t < NC; ++t) axpy4(acc[t], ds, kk[t]);
-            }
+            };
+#pragma unroll kUnroll<HP>
+            for (int jj = from; jj < to; ++jj) pair(jj);
         }
     }
     if (i < slots) store_row<NC>(dq + row * hd, acc, hd, r8);
 }
 
-template <int HP, typename T>
+template <int HP, typename T, bool SINKS>
 __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem p,
                                                                      const T* __restrict__ dout,
                                                                      const float* __restrict__ dsum,
                                                                      T* __restrict__ dk,
                                                                      T* __restrict__ dv) {
     constexpr int NC = HP / (4 * kLanesPerRow);
-    if (p.checked && p.checked->status != DEV_OK) return;
+    if (SINKS && p.checked->status != DEV_OK) return;
     extern __shared__ float4 bsm4[];
     float* qs = reinterpret_cast<float*>(bsm4);  // [kStage][HP]
     float* gs = qs + kStage * HP;                // [kStage][HP]
@@ -309,11 +316,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
             }
             __syncthreads();
             if (c0 + n <= wi0 || c0 >= wi1) continue;  // warp-uniform
-            // only what the warp's rows see of the chunk
-            const int from = wi0 > c0 ? static_cast<int>(wi0 - c0) : 0;
-            const int to = wi1 < c0 + n ? static_cast<int>(wi1 - c0) : n;
-#pragma unroll kUnroll<HP>
-            for (int ii = from; ii < to; ++ii) {
+            const auto pair = [&](int ii) {
                 const long long i = c0 + ii;
                 const float4* qr = reinterpret_cast<const float4*>(qs + ii * HP);
                 const float4* gr = reinterpret_cast<const float4*>(gs + ii * HP);
@@ -328,13 +331,23 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_dkdv_kernel(AttnProblem 
                 }
                 group_sum2(s, dp);
                 const float pij = (i >= i0 && i < i1) ? exp2f(fmaf(s, scale2, -ls[ii])) : 0.f;
-                const bool alone = p.checked && (i == lo || (p.window == 1 && p.sinks == 0));  // (as for dq)
+                const bool alone = SINKS && (i == lo || (p.window == 1 && p.sinks == 0));  // (as for dq)
                 const float dsv = alone ? 0.f : pij * (dp - dd[ii]) * p.scale;
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
                     axpy4(ak[t], dsv, qq[t]);
                     axpy4(av[t], pij, gg[t]);
                 }
+            };
+            if constexpr (HP == 128) {
+                // (registers are short: the bounds below cost 3 % without a window and give 2 % with one)
+                for (int ii = 0; ii < n; ++ii) pair(ii);
+            } else {
+                // only what the warp's rows see of the chunk
+                const int from = wi0 > c0 ? static_cast<int>(wi0 - c0) : 0;
+                const int to = wi1 < c0 + n ? static_cast<int>(wi1 - c0) : n;
+#pragma unroll kUnroll<HP>
+                for (int ii = from; ii < to; ++ii) pair(ii);
             }
         }
     }
@@ -493,24 +506,24 @@ __global__ void __launch_bounds__(256) attn_bwd_zero_outside_kernel(AttnProblem 
     }
 }
 
-template <int HP, typename T>
+template <int HP, typename T, bool SINKS>
 void launch_bwd_hp(const AttnProblem& p, const T* dout, const float* dsum, T* dq, T* dk, T* dv,
                    unsigned tiles, cudaStream_t stream) {
     const size_t smem_dq = 2 * static_cast<size_t>(kStage) * HP * sizeof(float);
     const size_t smem_kv = smem_dq + 2 * kStage * sizeof(float);
-    attn_bwd_dq_kernel<HP, T><<<dim3(tiles, p.heads), kBwdThreads, smem_dq, stream>>>(p, dout, dsum, dq);
-    attn_bwd_dkdv_kernel<HP, T><<<dim3(tiles, p.kv_heads), kBwdThreads, smem_kv, stream>>>(
+    attn_bwd_dq_kernel<HP, T, SINKS><<<dim3(tiles, p.heads), kBwdThreads, smem_dq, stream>>>(p, dout, dsum, dq);
+    attn_bwd_dkdv_kernel<HP, T, SINKS><<<dim3(tiles, p.kv_heads), kBwdThreads, smem_kv, stream>>>(
         p, dout, dsum, dk, dv);
 }
 
-template <typename T>
+template <typename T, bool SINKS>
 void launch_bwd_t(const AttnProblem& p, const void* dout, const float* dsum, void* dq, void* dk, void* dv,
                   unsigned tiles, cudaStream_t stream) {
     const T* go = static_cast<const T*>(dout);
     T *a = static_cast<T*>(dq), *b = static_cast<T*>(dk), *c = static_cast<T*>(dv);
-    if (p.head_dim <= 32) launch_bwd_hp<32>(p, go, dsum, a, b, c, tiles, stream);
-    else if (p.head_dim <= 64) launch_bwd_hp<64>(p, go, dsum, a, b, c, tiles, stream);
-    else launch_bwd_hp<128>(p, go, dsum, a, b, c, tiles, stream);
+    if (p.head_dim <= 32) launch_bwd_hp<32, T, SINKS>(p, go, dsum, a, b, c, tiles, stream);
+    else if (p.head_dim <= 64) launch_bwd_hp<64, T, SINKS>(p, go, dsum, a, b, c, tiles, stream);
+    else launch_bwd_hp<128, T, SINKS>(p, go, dsum, a, b, c, tiles, stream);
 }
 
 }  // namespace
@@ -548,10 +561,11 @@ cudaError_t launch_attn_bwd(const AttnProblem& p, const void* dout, const float*
                             void* dk, void* dv, int is_bf16, cudaStream_t stream) {
     const int64_t slots = static_cast<int64_t>(p.total_tokens) * p.slot_mult;
     if (slots == 0) return cudaSuccess;
-    if (p.head_dim > 128 || (p.sinks > 0 && is_bf16)) return cudaErrorInvalidValue;
+    if (p.head_dim > 128 || (p.checked && is_bf16)) return cudaErrorInvalidValue;
     const unsigned tiles = static_cast<unsigned>((slots + kRowsPerBlock - 1) / kRowsPerBlock);
-    if (is_bf16) launch_bwd_t<__nv_bfloat16>(p, dout, dsum, dq, dk, dv, tiles, stream);
-    else launch_bwd_t<float>(p, dout, dsum, dq, dk, dv, tiles, stream);
+    if (is_bf16) launch_bwd_t<__nv_bfloat16, false>(p, dout, dsum, dq, dk, dv, tiles, stream);
+    else if (p.checked) launch_bwd_t<float, true>(p, dout, dsum, dq, dk, dv, tiles, stream);
+    else launch_bwd_t<float, false>(p, dout, dsum, dq, dk, dv, tiles, stream);
     if (p.sinks > 0 && p.window > 0) {
         if (p.head_dim <= 32) launch_far<32>(p, dout, dsum, dk, dv, stream);
         else if (p.head_dim <= 64) launch_far<64>(p, dout, dsum, dk, dv, stream);
