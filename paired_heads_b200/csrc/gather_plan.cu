@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kPlanThreads) gather_plan_kernel(GatherProblem
     __syncthreads();
     const int code = bad && strict ? DEV_BAD_SEQLENS : (n_tiles > max_tiles ? DEV_OVERFLOW : DEV_OK);
     if (tid == 0) {
-        const int report = code != DEV_OK ? code : (bad ? DEV_BAD_SEQLENS : DEV_OK);
+        const int report = bad ? DEV_BAD_SEQLENS : code;  // (overlapping sequences, too many tiles: bad lengths first)
         p.hdr->n_items = code == DEV_OK ? static_cast<int>(n_tiles) : 0;
         p.hdr->status = report;
         if (p.status && report != DEV_OK) atomicMax(p.status, report);

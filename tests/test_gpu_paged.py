@@ -419,3 +419,17 @@ def test_more_sequences_than_a_grid_has_columns(pha, dtype, hd, q):
     o, lse = c.run(pha)
     assert c.status.item() == 1
     assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype,hd,q", [(BF16, 64, 1000), (BF16, 64, 4), (F32, 8, 40)])
+def test_sequences_that_overlap_are_reported(pha, dtype, hd, q):
+    """cu_seqlens that goes back and forth: more rows than q has, however they are counted. Status 1, and
+    nothing outside q's rows is written."""
+    c = Case((q,) + (0,) * 9, (q + 5,) * 10, 2, 1, hd, dtype, 16, max_q=q)
+    c.cu.copy_(torch.tensor([0, q] * 5 + [0]))
+    o = torch.full((q + 8, 2, hd), float("nan"), device="cuda").to(dtype)
+    lse = torch.full((q + 8, 2), float("nan"), device="cuda")
+    c.call(pha, o[4:-4], lse[4:-4], c.workspace(pha))
+    assert c.status.item() == 1
+    assert torch.isnan(o[:4]).all() and torch.isnan(o[-4:]).all()
+    assert torch.isnan(lse[:4]).all() and torch.isnan(lse[-4:]).all()
