@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         TileRec o{};
         uint64_t row_lse = 0, row_d = 0;  // query-major: this row's -lse * log2(e) and -D, twice
-        if (p.test_stall_us > 0)  // the wait runs out: status 3, and every role winds down
+        if (p.test_stall_us > 0)  // test hook, as in the band kernel: the wait runs out, status 3, every role winds down
             mbar_wait(&bars->stall, 0, abort_flag, dev_status, 1000ull * static_cast<uint64_t>(p.test_stall_us));
         else for (;; ++g) {
             {

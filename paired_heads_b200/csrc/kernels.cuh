@@ -84,8 +84,8 @@ struct AttnProblem {
     // Value embedding (pha_attn_fwd_aux_v): added to v, with v's layout, before attention;
     // nullptr: none.
     const void* v_aux;
-    // Failure-detection test hook (band kernel, backward with sinks): > 0 makes the softmax warps first
-    // wait up to this many microseconds on a barrier that nothing signals; 0 in every normal call.
+    // Failure-detection test hook (band kernel): > 0 makes the softmax warps first wait up to this
+    // many microseconds on a barrier that nothing signals; 0 in every normal call.
     int test_stall_us;
     // FP8 inputs (pha_attn_fwd_fp8): q, k, v hold e4m3 codes standing for qk / v scale times
     // their values; the block kernel folds qk_scale (= q_scale * k_scale) into the logit scale
