@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const __nv_bfloat16* k_all = static_cast<const __nv_bfloat16*>(p.k) + unit * 8;
         const __nv_bfloat16* v_all = static_cast<const __nv_bfloat16*>(p.v) + unit * 8;
         const bool q_boxes = kBlockM % p.pack == 0;
-        uint32_t qc = 0, kc = 0, vc = 0;  // Q sub-tiles, K tiles and V tiles issued
+        uint32_t qc = 0, kc = 0;  // Q sub-tiles and key tiles issued
+        uint32_t k_alone = 0;     // giving up: K of one tile more
         bool ok = true;
         auto acquire = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status));
@@ -412,9 +413,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int head = it.chunk * p.pack / G;
             if (w == 0) ok = publish(&it);
             if (ok && it.active(0)) ok = load_q(it, 0);
-            for (int t = it.tb; ok && t < it.te; ++t) {
+            for (int t = it.tb; ok && t < it.te; ++t, ++kc) {
                 const int col0 = t * kBlockN;
-                const uint32_t sk = kc % L::kKStages, sv = vc % L::kVStages;
+                const uint32_t sk = kc % L::kKStages, sv = kc % L::kVStages;
                 // all 128 columns are window columns, or tokens of the sequence behind the last one
                 const int past = col0 + kBlockN - it.cols.n_w;
                 if (p.box_rows >= 8 && (past <= 0 || (it.cols.total == it.cols.n_w && past <= it.behind))) {
@@ -422,12 +423,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!ok) break;
                     if (w == 0) load_boxes(&tm_k, L::kOffK + sk * L::kKV, it, col0, head, &bars->k_full[sk]);
                     else mbar_arrive(&bars->k_full[sk]);
-                    ++kc;
-                    ok = acquire(&bars->v_empty[sv], ((vc / L::kVStages) & 1) ^ 1);
-                    if (!ok) break;
+                    ok = acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
+                    if (!ok) {
+                        k_alone = 1;
+                        break;
+                    }
                     if (w == 1) load_boxes(&tm_v, L::kOffV + sv * L::kKV, it, col0, head, &bars->v_full[sv]);
                     else mbar_arrive(&bars->v_full[sv]);
-                    ++vc;
                 } else {
                     // documents: whole groups of 8 window columns by TMA, the rest row by row. (Pages: the lookups in
                     // between made it slower, 68 us instead of 63 for 24 sequences of 1 to 300 new tokens, 12 heads
@@ -452,14 +454,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         load_groups(&tm_k8, L::kOffK + sk * L::kKV, it.where + it.cols.lo + col0, groups, head, &bars->k_full[sk]);
                     load_rows(sbase + L::kOffK + sk * L::kKV, k_all, 8 * groups, idx[0], idx[1], idx[2], idx[3], head);
                     cp_async_arrive(&bars->k_full[sk]);
-                    ++kc;
-                    ok = acquire(&bars->v_empty[sv], ((vc / L::kVStages) & 1) ^ 1);
-                    if (!ok) break;
+                    ok = acquire(&bars->v_empty[sv], ((kc / L::kVStages) & 1) ^ 1);
+                    if (!ok) {
+                        k_alone = 1;
+                        break;
+                    }
                     if (!PAGED && w == 1)
                         load_groups(&tm_v8, L::kOffV + sv * L::kKV, it.where + it.cols.lo + col0, groups, head, &bars->v_full[sv]);
                     load_rows(sbase + L::kOffV + sv * L::kKV, v_all, 8 * groups, idx[0], idx[1], idx[2], idx[3], head);
                     cp_async_arrive(&bars->v_full[sv]);
-                    ++vc;
                 }
                 // the second sub-tile's Q after the first key tile: its slot is free only when the previous
                 // item's epilogue is through, and the first sub-tile can start without it
@@ -477,8 +480,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     while (!mbar_test(&bars_of[n % ring], (n / ring) & 1) && globaltimer_ns() - t0 <= kWaitLimitNs) {}
             };
             drain(bars->q_full, L::kQSlots, qc);
-            drain(bars->k_full, L::kKStages, kc);
-            drain(bars->v_full, L::kVStages, vc);
+            drain(bars->k_full, L::kKStages, kc + k_alone);
+            drain(bars->v_full, L::kVStages, kc);
         }
         __syncwarp();
     } else if (warp == 8) {
