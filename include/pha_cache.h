@@ -101,8 +101,9 @@ pha_status pha_test_attn_paged_fwd_stalled(const void* q, const void* k_pages, c
 /*
  * pha_cache_append -- writes the new tokens' keys and values (rotated already: pha_rope) to their
  *   places in one layer's pages. k, v: [total][n_kv_heads][head_dim]; cu_seqlens, kv_lens (new
- *   tokens included), page_table as pha_attn_paged_fwd. Any type: element_bytes is 1, 2 or 4, and
- *   n_kv_heads * head_dim * element_bytes a multiple of 16.
+ *   tokens included), page_table as pha_attn_paged_fwd. Any type: element_bytes is 1, 2 or 4 (1 for
+ *   caches that other code reads: pha_attn_paged_fwd takes bf16 and f32), and n_kv_heads * head_dim *
+ *   element_bytes a multiple of 16.
  *   A token whose place is out of range (status 1) or whose entry is no page (status 4) is left out.
  *   No two tokens may have one place (pages shared by sequences are not written: pha_cache_reserve
  *   copies the one a sequence grows into).
